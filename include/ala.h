@@ -119,14 +119,16 @@ ALA_API void ala_op_destroy(ala_op* op);
  * replace the schedule this op's executions read) and that it stays
  * allocated; binding a NULL workspace unbinds.  Status: ALA_NULL_REQUIRED (op NULL),
  * ALA_WORKSPACE_TOO_SMALL, ALA_INVALID_PARAM (misaligned: 16 bytes for the
- * prefill ops, 256 for MLA), ALA_CUDA_ERROR. */
+ * prefill ops, 256 for MLA and the paged ops), ALA_CUDA_ERROR. */
 ALA_API int ala_op_bind_workspace(ala_op* op, void* workspace, uint64_t workspaceSize, ala_stream_t stream);
 
 /* Reads the device status word of `workspace` for `op` (synchronous copy on
  * the legacy stream after synchronising `stream`).  *code = 0 means every
  * kernel wait completed; 0x101..0x10A identifies the wait that ran out; 0x10B
- * (range-checking build libala_debug.so only) means a block-table entry that
- * was read lay outside [0, numBlocks): that page was read as zeros. */
+ * (the paged ops with device lengths; of the others the range-checking build
+ * libala_debug.so only) means a block-table entry that was read lay outside
+ * [0, numBlocks): that page was read as zeros; 0x10C (paged ops) that a
+ * device length was out of range and was cut. */
 ALA_API int ala_workspace_status(const ala_op* op, const void* workspace, ala_stream_t stream, int32_t* code);
 
 /* ---------------------------------------------------------------------------
@@ -313,6 +315,146 @@ ALA_API int atb_like_mla(void* workspace, uint64_t workspaceSize, ala_op* op, al
  * ------------------------------------------------------------------------- */
 ALA_API int ala_lse_merge(const ala_tensor* outA, const ala_tensor* lseA, const ala_tensor* outB,
                           const ala_tensor* lseB, ala_tensor* out, ala_tensor* lse, ala_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged serving: one decoding step over a paged cache with every length in
+ * DEVICE memory, so that the same planned calls (or one captured graph of
+ * them) serve every step.  The pages take host lengths and have no
+ * counterpart.  In the order of a step:
+ *   ala_paged_step            block tables, slot map, positions, lengths
+ *   ala_paged_write           the step's K / V rows into the cache
+ *   ala_paged_attention       attention of the new tokens over the cache
+ *   ala_paged_diff_attention  the same with two softmax maps per head
+ * Rows of every tensor are dense; queries and new K / V rows may be slices of
+ * a wider row (a fused projection) through a stride between tokens, counted
+ * in elements, 0 meaning dense.  `stream` must belong to the device of the
+ * tensors, and that device must be current.
+ * ------------------------------------------------------------------------- */
+
+/* Codes that ala_paged_step leaves in `status`. */
+enum {
+  ALA_STEP_OK = 0,
+  ALA_STEP_BAD_LENGTH = 1,      /* a negative length, or one past maxBlockNum blocks                 */
+  ALA_STEP_TOO_MANY_TOKENS = 2, /* sum(seqLen) > nTokens                                             */
+  ALA_STEP_BAD_FREE_COUNT = 3,  /* freeCount < 0, or it and the returned blocks exceed numBlocks     */
+  ALA_STEP_OUT_OF_BLOCKS = 4,   /* the free blocks do not cover the new tokens                       */
+  ALA_STEP_BAD_BLOCK = 5        /* a block used lies outside [0, numBlocks): tokens in it have slot -1 */
+};
+
+/* All tensors int32, device.
+ * seqLen      [batch] new tokens per request (0: idle).
+ * contextLens [batch] keys cached before the step.
+ * finished    NULL or [batch]: nonzero for a request that has ended.  Its
+ *             blocks return to the stack, and its row starts again empty
+ *             (with seqLen > 0: as a new request).
+ * blockTables [batch, maxBlockNum], updated: entries from
+ *             ceil(contextLens_b / blockSize) on are filled with new blocks.
+ *             Entries past a request's blocks are neither read nor written.
+ * freeBlocks  [numBlocks], updated: a stack of free blocks, the first
+ *             freeCount entries.  First the blocks of ended requests go onto
+ *             it, in request order and each request's in table order; then
+ *             new blocks come off its top, in request order.
+ * freeCount   [1].    blockSize > 0.
+ * Outputs:
+ * kvSeqLen    [batch] keys after the step.  May be contextLens itself.
+ * freeCountOut [1].   May be freeCount itself.
+ * cuSeqLen    [batch + 1] exclusive sums of seqLen.
+ * slotMapping [nTokens] cache row of each packed token (block * blockSize +
+ *             offset); -1 from sum(seqLen) on.
+ * positions   [nTokens] position of each token in its request; 0 from
+ *             sum(seqLen) on.
+ * status      [1] one of ALA_STEP_*.  With codes 1 to 4 the step changed
+ *             nothing: kvSeqLen = contextLens, freeCountOut = freeCount,
+ *             cuSeqLen and positions are 0 and every slot is -1 (a write with
+ *             them stores nothing).
+ * Limits: batch <= 8192; maxBlockNum * blockSize, numBlocks * blockSize and
+ * nTokens <= 2^30.  No other memory may be shared between the tensors.
+ * Asynchronous on `stream`, one launch, no workspace. */
+ALA_API int ala_paged_step(const ala_tensor* seqLen, const ala_tensor* contextLens, const ala_tensor* finished,
+                           ala_tensor* blockTables, ala_tensor* freeBlocks, const ala_tensor* freeCount,
+                           int32_t blockSize, ala_tensor* kvSeqLen, ala_tensor* freeCountOut, ala_tensor* cuSeqLen,
+                           ala_tensor* slotMapping, ala_tensor* positions, ala_tensor* status, ala_stream_t stream);
+
+/* key         [nTokens, row] or [nTokens, heads, headSize], device; any dtype.
+ * keyStride   elements between tokens (0: dense).
+ * value, valueStride  like key, with a row size and dtype of their own (a
+ *             latent cache and its rope keys, for instance); or NULL.
+ * slotMapping [nTokens] int32, device.  Token t's rows go to cache row
+ *             slotMapping[t]; values outside [0, numBlocks * blockSize) are
+ *             skipped.  A slot may appear once: with repeats, its row holds
+ *             a mixture of theirs.
+ * keyCache    [numBlocks, blockSize, row] or [numBlocks, blockSize, heads,
+ *             headSize], key's dtype, at most 2^30 rows; valueCache alike
+ *             (NULL with value).  Neither may overlap key or value.
+ * Asynchronous on `stream`, one launch, no workspace. */
+ALA_API int ala_paged_write(const ala_tensor* key, int64_t keyStride, const ala_tensor* value, int64_t valueStride,
+                            const ala_tensor* slotMapping, ala_tensor* keyCache, ala_tensor* valueCache,
+                            ala_stream_t stream);
+
+/* O = softmax(qkScale Q K^T + M) V of each sequence's new tokens over its
+ * paged keys: one token, a few, or a chunk, mixed in one batch.
+ *
+ * query, key, value, blockTables, slopes, headNum, kvHeadNum, qkScale and
+ *             attnOut as for the PrefixEncoder (f16/bf16; blockSize a
+ *             multiple of 16; headSize a multiple of 8 up to 256, up to 128
+ *             with ALiBi; at most 128 query heads per kv head), query and
+ *             caches 16-byte aligned, queryStride a multiple of 8.
+ * seqLen      [batch] int32, DEVICE: new tokens, packed in query in batch
+ *             order.  nTokens may be larger than their sum: rows behind the
+ *             last sequence are left as they were, in attnOut and in lse.
+ * kvSeqLen    [batch] int32, DEVICE: keys, the new tokens being the last.
+ * maskType    0, 3, 4, 5 or 9 (0: every key; the others: key j <= i +
+ *             kvSeqLen_b - seqLen_b for new token i).
+ * lse         NULL or [nTokens, headNum] (or [..., 1]) fp32, device.
+ *
+ * A row without a key (kvSeqLen 0, or kvSeqLen < seqLen) gets output 0 and
+ * lse -inf.  Slots past kvSeqLen may hold anything, NaN included; rows within
+ * kvSeqLen must be finite.
+ * Lengths are checked on the device: a negative one counts as 0, new tokens
+ * past nTokens are dropped, keys past maxBlockNum blocks too, and
+ * ala_workspace_status then reports 0x10C; a block-table entry in use outside
+ * [0, numBlocks) reads as zeros and reports 0x10B.  Both leave later
+ * executions unaffected.
+ * Results do not depend on which execution or graph replay computes them
+ * (no atomics in sums), but may differ in rounding with the other sequences
+ * of the batch, which decide where a long row is split.
+ * workspace   256-byte aligned; its size depends on headSize alone.  Two
+ *             executions that may overlap in time need two workspaces.  Once
+ *             bound (ala_op_bind_workspace) an execution is two kernel
+ *             launches; unbound, a 256-byte clear precedes them.  Both forms
+ *             may be captured into a graph (the binding itself may not). */
+ALA_API int ala_paged_attention_get_workspace_size(
+    const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
+    const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* slopes,
+    int maskType, int32_t headNum, int32_t kvHeadNum, float qkScale, ala_tensor* attnOut, ala_tensor* lse,
+    uint64_t* workspaceSize, ala_op** op);
+
+ALA_API int ala_paged_attention(void* workspace, uint64_t workspaceSize, ala_op* op, ala_stream_t stream);
+
+/* Differential attention: with two softmax maps P1, P2 per head,
+ *   O = (P1 - lambda_h P2) V,   P_m = softmax(qkScale Q_m K_m^T + M),
+ * then, with normWeight, a root-mean-square norm over each head's row, and
+ * outScale in either case:
+ *   O <- outScale * O / sqrt(mean(O^2) + normEps) * normWeight.
+ *
+ * query       [nTokens, 2 * headNum * headSize] or [nTokens, 2 * headNum,
+ *             headSize]: head h's two queries are heads 2h and 2h + 1.
+ * key         [numBlocks, blockSize, 2 * kvHeadNum, headSize] (or its last two
+ *             dims joined): kv head g's two keys are heads 2g and 2g + 1.
+ * value       [numBlocks, blockSize, kvHeadNum, 2 * headSize] (or joined).
+ * attnOut     [nTokens, headNum, 2 * headSize] (or joined).
+ * lambda      [headNum] fp32, device.
+ * normWeight  NULL or [2 * headSize] fp32, device;  normEps >= 0.
+ * maskType    0 or 9;  headSize a multiple of 8 up to 128; at most 64 heads
+ *             per kv head.
+ * Everything else as for ala_paged_attention; a row without a key gets 0. */
+ALA_API int ala_paged_diff_attention_get_workspace_size(
+    const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
+    const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* lambda,
+    const ala_tensor* normWeight, float normEps, float outScale, int maskType, int32_t headNum, int32_t kvHeadNum,
+    float qkScale, ala_tensor* attnOut, uint64_t* workspaceSize, ala_op** op);
+
+ALA_API int ala_paged_diff_attention(void* workspace, uint64_t workspaceSize, ala_op* op, ala_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -8,14 +8,23 @@ Entry points (names as in the C ABI):
   * ``varlen_attention``         contiguous packed K/V, mask types 0/3/4/5/9
   * ``atb_like_prefix_encoder``  paged K/V through blockTables, mask types 3/4/5/9
   * ``atb_like_mla``             MLA decode / speculative decode over a paged latent cache
+  * ``paged_step``               block tables, slot map, positions and lengths of a serving step, on the device
+  * ``paged_write``              a step's new K / V rows into the paged cache
+  * ``paged_attention``          attention of one, a few or a chunk of new tokens over the paged cache, with
+                                 every length read on the device
+  * ``paged_diff_attention``     the same with two softmax maps per head (differential attention)
 
-Each returns an ``Op`` that owns the workspace and can be executed again on
-the current CUDA stream (``op()``), which is what the bench does.
+Each has a ``plan_*`` form that returns an object (an ``Op``, which owns its
+workspace, where the call needs one) that runs the call again on the current
+CUDA stream (``op()``), which is what the bench does.  A planned paged call
+reads its lengths on the device, so one plan, or one CUDA graph of several,
+serves every step of a server; calls of one ``Op`` must not overlap in time.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -29,6 +38,8 @@ MASK_NONE, MASK_ALIBI, MASK_ALIBI_SQRT, MASK_ALIBI_LEFT, MASK_CAUSAL = 0, 3, 4, 
 MLA_MASK_UNDEFINED, MLA_MASK_SPEC, MLA_MASK_FREE = 0, 1, 2
 MLA_CALC_UNDEFINED, MLA_CALC_SPEC, MLA_CALC_RING, MLA_CALC_PREFILL = 0, 1, 2, 3
 MLA_CACHE_KVCACHE, MLA_CACHE_KROPE_CTKV, MLA_CACHE_INT8_NZ, MLA_CACHE_NZ = 0, 1, 2, 3
+
+STEP_OK, STEP_BAD_LENGTH, STEP_TOO_MANY_TOKENS, STEP_BAD_FREE_COUNT, STEP_OUT_OF_BLOCKS, STEP_BAD_BLOCK = range(6)
 
 STATUS = {0: "OK", 1: "NULL_REQUIRED", 2: "INVALID_SHAPE", 3: "INVALID_DTYPE", 4: "INVALID_PARAM",
           5: "UNSUPPORTED", 6: "WORKSPACE_TOO_SMALL", 7: "CUDA_ERROR", 8: "DEVICE_TIMEOUT"}
@@ -87,11 +98,24 @@ def lib() -> ctypes.CDLL:
         L.ala_op_bind_workspace.restype = ctypes.c_int
         L.ala_lse_merge.argtypes = [T, T, T, T, T, T, P]
         L.ala_lse_merge.restype = ctypes.c_int
-        for f in ("atb_like_prefix_encoder", "varlen_attention", "atb_like_mla"):
+        I64 = ctypes.c_int64
+        L.ala_paged_step.argtypes = [T, T, T, T, T, T, ctypes.c_int32, T, T, T, T, T, T, P]
+        L.ala_paged_write.argtypes = [T, I64, T, I64, T, T, T, P]
+        L.ala_paged_attention_get_workspace_size.argtypes = [T, I64, T, T, T, T, T, T, ctypes.c_int, ctypes.c_int32,
+                                                             ctypes.c_int32, ctypes.c_float, T, T, U64P, OPP]
+        L.ala_paged_diff_attention_get_workspace_size.argtypes = [T, I64, T, T, T, T, T, T, T, ctypes.c_float,
+                                                                  ctypes.c_float, ctypes.c_int, ctypes.c_int32,
+                                                                  ctypes.c_int32, ctypes.c_float, T, U64P, OPP]
+        for f in ("ala_paged_step", "ala_paged_write", "ala_paged_attention_get_workspace_size",
+                  "ala_paged_diff_attention_get_workspace_size"):
+            getattr(L, f).restype = ctypes.c_int
+        for f in ("atb_like_prefix_encoder", "varlen_attention", "atb_like_mla", "ala_paged_attention",
+                  "ala_paged_diff_attention"):
             getattr(L, f).argtypes = [P, ctypes.c_uint64, P, P]
         for f in ("ala_workspace_status", "atb_like_prefix_encoder_get_workspace_size",
                   "varlen_attention_get_workspace_size", "atb_like_mla_get_workspace_size",
-                  "atb_like_prefix_encoder", "varlen_attention", "atb_like_mla"):
+                  "atb_like_prefix_encoder", "varlen_attention", "atb_like_mla", "ala_paged_attention",
+                  "ala_paged_diff_attention"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -308,3 +332,185 @@ def lse_merge(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None):
     ts = [tensor(out_a), tensor(lse_a), tensor(out_b), tensor(lse_b), tensor(out), tensor(lse)]
     _check(L.ala_lse_merge(*[_ref(t) for t in ts], ctypes.c_void_p(s.cuda_stream)))
     return out, lse
+
+
+# ---------------------------------------------------------------------------- paged serving, lengths on the device
+
+def _rows(x, name: str):
+    """(ala_tensor, elements between rows) of a [tokens, ...] tensor whose rows are dense: a slice of a wider
+    row (a fused projection) needs no copy."""
+    if x is None:
+        return None, 0
+    row = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != row:
+            raise ValueError(f"{name}: each token's row must be dense")
+        row *= size
+    stride = x.stride(0) if x.shape[0] > 1 else row
+    if stride < row:
+        raise ValueError(f"{name}: tokens overlap")
+    t = AlaTensor()
+    t.data, t.dtype, t.ndim = x.data_ptr(), _TORCH_DTYPE[x.dtype], x.dim()
+    for i, s in enumerate(x.shape):
+        t.dims[i] = s
+    return t, stride
+
+
+def _same_device(first, **tensors):
+    for name, x in tensors.items():
+        if x is not None and x.device != first.device:
+            raise ValueError(f"{name} is on {x.device}, not on {first.device}")
+
+
+def _launch(device, stream, call):
+    """call(stream handle) with `device` current; raises the library's error."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(call(s.cuda_stream))
+    else:
+        _check(call(s.cuda_stream))
+
+
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+class PagedOp(Op):
+    """A planned paged attention call.  Its first execution binds the workspace (a synchronisation), unless the
+    stream is being captured; a captured execution needs no binding."""
+
+    def __call__(self, stream: torch.cuda.Stream | None = None):
+        if not self._bound and not _capturing(stream):
+            _launch(self.workspace.device, stream, lambda s: lib().ala_op_bind_workspace(
+                self._handle, self.workspace.data_ptr(), self.workspace_size, s))
+            self._bound = True
+        _launch(self.workspace.device, stream,
+                lambda s: self._execute(self.workspace.data_ptr(), self.workspace_size, self._handle, s))
+        return self
+
+
+class PagedCall:
+    """A planned call that needs no workspace: call it to run on the current stream."""
+
+    def __init__(self, function, args, device, keep):
+        self._function, self._args, self._device, self._keep = function, args, device, keep
+
+    def __call__(self, stream: torch.cuda.Stream | None = None):
+        _launch(self._device, stream, lambda s: self._function(*self._args, s))
+        return self
+
+
+class StepOutputs(NamedTuple):
+    """What a step leaves on the device (ala_paged_step)."""
+    kv_seq_len: torch.Tensor    # [batch]
+    free_count: torch.Tensor    # [1]
+    cu_seq_len: torch.Tensor    # [batch + 1]
+    slot_mapping: torch.Tensor  # [n_tokens]
+    positions: torch.Tensor     # [n_tokens]
+    status: torch.Tensor        # [1], STEP_*
+
+
+def plan_paged_step(seq_len, context_lens, block_tables, free_blocks, free_count, block_size, n_tokens, finished=None,
+                    kv_seq_len=None, free_count_out=None) -> tuple[PagedCall, StepOutputs]:
+    """Plan a serving step's bookkeeping; returns (call, outputs).  Every tensor is int32 on the device;
+    ``block_tables`` and ``free_blocks`` are updated in place.  A server that passes ``kv_seq_len=context_lens``
+    and ``free_count_out=free_count`` carries its state from step to step on the device."""
+    dev = seq_len.device
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
+    out = StepOutputs(new(seq_len.shape[0]) if kv_seq_len is None else kv_seq_len,
+                      new(1) if free_count_out is None else free_count_out, new(block_tables.shape[0] + 1),
+                      new(int(n_tokens)), new(int(n_tokens)), new(1))
+    _same_device(seq_len, context_lens=context_lens, block_tables=block_tables, free_blocks=free_blocks,
+                 free_count=free_count, finished=finished, kv_seq_len=out.kv_seq_len, free_count_out=out.free_count)
+    ins = [tensor(x) for x in (seq_len, context_lens, finished, block_tables, free_blocks, free_count)]
+    outs = [tensor(x) for x in out]
+    args = (*[_ref(t) for t in ins], int(block_size), *[_ref(t) for t in outs])
+    keep = (seq_len, context_lens, finished, block_tables, free_blocks, free_count, out, ins, outs)
+    return PagedCall(lib().ala_paged_step, args, dev, keep), out
+
+
+def paged_step(seq_len, context_lens, block_tables, free_blocks, free_count, block_size, n_tokens, finished=None,
+               kv_seq_len=None, free_count_out=None) -> StepOutputs:
+    call, out = plan_paged_step(seq_len, context_lens, block_tables, free_blocks, free_count, block_size, n_tokens,
+                                finished, kv_seq_len, free_count_out)
+    call()
+    return out
+
+
+def plan_paged_write(key, value, slot_mapping, key_cache, value_cache) -> PagedCall:
+    """Plan the store of new K / V rows ([tokens, heads, d]; tokens may lie apart, as in a slice of a fused
+    projection) into the caches by slot.  ``value`` and ``value_cache`` may both be None."""
+    _same_device(key, value=value, slot_mapping=slot_mapping, key_cache=key_cache, value_cache=value_cache)
+    (tk, sk), (tv, sv) = _rows(key, "key"), _rows(value, "value")
+    ts, tkc, tvc = tensor(slot_mapping), tensor(key_cache), tensor(value_cache)
+    args = (_ref(tk), sk, _ref(tv), sv, _ref(ts), _ref(tkc), _ref(tvc))
+    return PagedCall(lib().ala_paged_write, args, key.device, (key, value, slot_mapping, key_cache, value_cache, tk, tv, ts, tkc, tvc))
+
+
+def paged_write(key, value, slot_mapping, key_cache, value_cache):
+    plan_paged_write(key, value, slot_mapping, key_cache, value_cache)()
+
+
+def plan_paged_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, mask_type, heads, kv_heads, qk_scale,
+                         slopes=None, out=None, lse=None) -> tuple[PagedOp, torch.Tensor]:
+    """Plan attention of the packed new tokens ``q`` over their paged keys; returns (op, out).  ``seq_len`` and
+    ``kv_seq_len`` are device tensors that each execution reads, so one op serves every step.  Rows of ``out``
+    and ``lse`` behind the last sequence are left as they were."""
+    L = lib()
+    out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_len=seq_len, kv_seq_len=kv_seq_len,
+                 slopes=slopes, out=out, lse=lse)
+    tq, stride = _rows(q, "q")
+    ts = [tensor(x) for x in (k_cache, v_cache, block_tables, seq_len, kv_seq_len, slopes)]
+    ws, h = ctypes.c_uint64(0), ctypes.c_void_p(0)
+    _check(L.ala_paged_attention_get_workspace_size(_ref(tq), stride, *[_ref(t) for t in ts], int(mask_type), int(heads),
+                                                    int(kv_heads), float(qk_scale), _ref(tensor(out)),
+                                                    _ref(tensor(lse)), ctypes.byref(ws), ctypes.byref(h)))
+    return PagedOp(h, ws.value, L.ala_paged_attention, q.device,
+                   (q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, slopes, out, lse)), out
+
+
+def paged_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, mask_type, heads, kv_heads, qk_scale,
+                    slopes=None, return_lse=False):
+    lse = (torch.full((q.shape[0], heads), float("-inf"), dtype=torch.float32, device=q.device)
+           if return_lse else None)
+    op, out = plan_paged_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, mask_type, heads, kv_heads,
+                                   qk_scale, slopes, lse=lse)
+    op()
+    return (out, lse) if return_lse else out
+
+
+def plan_paged_diff_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, lam, mask_type, heads, kv_heads,
+                              qk_scale, norm_weight=None, norm_eps=1e-5, out_scale=1.0,
+                              out=None) -> tuple[PagedOp, torch.Tensor]:
+    """Plan differential attention (softmax map 1 minus ``lam`` times softmax map 2) of the packed new tokens;
+    returns (op, out).  q [tokens, 2 heads, d], k_cache [..., 2 kv_heads, d], v_cache [..., kv_heads, 2 d],
+    lam [heads] fp32, out [tokens, heads, 2 d]; with ``norm_weight`` ([2 d] fp32) an RMS norm of each head's row
+    follows, and ``out_scale`` multiplies the result."""
+    L = lib()
+    if out is None:
+        d2 = q.shape[-1] * 2 if q.dim() == 3 else q.shape[-1] // int(heads)
+        out = torch.zeros((q.shape[0], int(heads), d2), dtype=q.dtype, device=q.device)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_len=seq_len, kv_seq_len=kv_seq_len,
+                 lam=lam, norm_weight=norm_weight, out=out)
+    tq, stride = _rows(q, "q")
+    ts = [tensor(x) for x in (k_cache, v_cache, block_tables, seq_len, kv_seq_len, lam, norm_weight)]
+    ws, h = ctypes.c_uint64(0), ctypes.c_void_p(0)
+    _check(L.ala_paged_diff_attention_get_workspace_size(_ref(tq), stride, *[_ref(t) for t in ts], float(norm_eps),
+                                                         float(out_scale), int(mask_type), int(heads), int(kv_heads),
+                                                         float(qk_scale), _ref(tensor(out)), ctypes.byref(ws),
+                                                         ctypes.byref(h)))
+    return PagedOp(h, ws.value, L.ala_paged_diff_attention, q.device,
+                   (q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, lam, norm_weight, out)), out
+
+
+def paged_diff_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, lam, mask_type, heads, kv_heads,
+                         qk_scale, norm_weight=None, norm_eps=1e-5, out_scale=1.0):
+    op, out = plan_paged_diff_attention(q, k_cache, v_cache, block_tables, seq_len, kv_seq_len, lam, mask_type, heads,
+                                        kv_heads, qk_scale, norm_weight, norm_eps, out_scale)
+    op()
+    return out

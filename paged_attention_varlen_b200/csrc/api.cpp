@@ -14,6 +14,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <new>
 #include <queue>
 #include <string>
 #include <utility>
@@ -22,6 +23,7 @@
 #include "../../include/ala.h"
 #include "internal.h"
 #include "mla.h"
+#include "paged.h"
 
 using namespace ala;
 
@@ -131,7 +133,7 @@ struct PinnedImage {
 };
 
 struct ala_op {
-  enum Kind { kPrefill, kMla } kind = kPrefill;
+  enum Kind { kPrefill, kMla, kPagedAttn, kPagedDiff } kind = kPrefill;
   // prefill
   int32_t dtype = 0, heads = 0, kv_heads = 0, head_size = 0, mask_type = 0, batch = 0;
   float qk_scale = 1.f;
@@ -151,6 +153,8 @@ struct ala_op {
   const void* bound_ws = nullptr;  // a workspace that holds this op's schedule (ala_op_bind_workspace)
   // mla
   MlaPlan mla;
+  // paged attention with device lengths
+  PagedPlan paged_attn;
 };
 
 extern "C" const char* ala_last_error(void) { return g_last_error.c_str(); }
@@ -169,19 +173,25 @@ extern "C" int ala_op_bind_workspace(ala_op* op, void* workspace, uint64_t works
   if (!workspace) {  // unbind
     op->bound_ws = nullptr;
     op->mla.bound_ws = nullptr;
+    op->paged_attn.bound_ws = nullptr;
     return ok();
   }
   const bool mla = op->kind == ala_op::kMla;
-  const uint64_t need = mla ? op->mla.ws_size : op->ws_size;
+  const bool paged = op->kind == ala_op::kPagedAttn || op->kind == ala_op::kPagedDiff;
+  const uint64_t need = mla ? op->mla.ws_size : paged ? op->paged_attn.ws_size : op->ws_size;
   if (workspaceSize < need)
     return fail(ALA_WORKSPACE_TOO_SMALL, "%s: workspace %llu < required %llu", fn, (unsigned long long)workspaceSize,
                 (unsigned long long)need);
-  if (reinterpret_cast<uintptr_t>(workspace) % (mla ? 256 : 16))
-    return fail(ALA_INVALID_PARAM, "%s: workspace must be %d-byte aligned", fn, mla ? 256 : 16);
+  if (reinterpret_cast<uintptr_t>(workspace) % (mla || paged ? 256 : 16))
+    return fail(ALA_INVALID_PARAM, "%s: workspace must be %d-byte aligned", fn, mla || paged ? 256 : 16);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   op->bound_ws = nullptr;
   op->mla.bound_ws = nullptr;
-  if (mla) {
+  op->paged_attn.bound_ws = nullptr;
+  if (paged) {  // no schedule: only the status words have an initial value
+    if (cudaMemsetAsync(workspace, 0, kPagedStatusBytes, st) != cudaSuccess)
+      return fail(ALA_CUDA_ERROR, "%s: status clear failed: %s", fn, cudaGetErrorString(cudaGetLastError()));
+  } else if (mla) {
     char err[512] = {0};
     const int s = mla_upload(&op->mla, workspace, st, err, sizeof err);
     if (s != ALA_OK) return fail(s, "%s: %s", fn, err);
@@ -193,6 +203,7 @@ extern "C" int ala_op_bind_workspace(ala_op* op, void* workspace, uint64_t works
   if (cudaStreamSynchronize(st) != cudaSuccess)
     return fail(ALA_CUDA_ERROR, "%s: stream sync failed: %s", fn, cudaGetErrorString(cudaGetLastError()));
   if (mla) op->mla.bound_ws = workspace;
+  else if (paged) op->paged_attn.bound_ws = workspace;
   else op->bound_ws = workspace;
   return ok();
 }
@@ -658,4 +669,102 @@ extern "C" int ala_lse_merge(const ala_tensor* outA, const ala_tensor* lseA, con
                                               reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(ALA_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
   return ok();
+}
+
+// ------------------------------------------------------------------ paged attention, lengths on the device
+namespace {
+
+int plan_paged(const PagedAttnArgs& a, uint64_t* workspaceSize, ala_op** op, const char* fn) {
+  if (!workspaceSize || !op) return fail(ALA_NULL_REQUIRED, "%s: workspaceSize and op are required", fn);
+  *op = nullptr;
+  PagedPlan plan;
+  char err[512] = {0};
+  const int st = paged_plan(&plan, a, err, sizeof err);
+  if (st != ALA_OK) return fail(st, "%s: %s", fn, err);
+  ala_op* o = new (std::nothrow) ala_op();
+  if (!o) return fail(ALA_INVALID_PARAM, "%s: out of host memory", fn);
+  o->kind = a.diff ? ala_op::kPagedDiff : ala_op::kPagedAttn;
+  o->paged_attn = plan;
+  *workspaceSize = plan.ws_size;
+  *op = o;
+  return ok();
+}
+
+int run_paged(void* workspace, uint64_t workspaceSize, ala_op* op, ala_stream_t stream, ala_op::Kind kind, const char* fn) {
+  if (!op) return fail(ALA_NULL_REQUIRED, "%s: op is NULL", fn);
+  if (op->kind != kind) return fail(ALA_INVALID_PARAM, "%s: op was not made by %s_get_workspace_size", fn, fn);
+  if (!workspace) return fail(ALA_NULL_REQUIRED, "%s: workspace is NULL", fn);
+  if (workspaceSize < op->paged_attn.ws_size)
+    return fail(ALA_WORKSPACE_TOO_SMALL, "%s: workspace %llu < required %llu", fn, (unsigned long long)workspaceSize,
+                (unsigned long long)op->paged_attn.ws_size);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(ALA_INVALID_PARAM, "%s: workspace must be 256-byte aligned", fn);
+  char err[512] = {0};
+  const int st = paged_run(&op->paged_attn, workspace, reinterpret_cast<cudaStream_t>(stream), err, sizeof err);
+  if (st != ALA_OK) return fail(st, "%s: %s", fn, err);
+  return ok();
+}
+
+}  // namespace
+
+extern "C" int ala_paged_attention_get_workspace_size(
+    const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
+    const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* slopes,
+    int maskType, int32_t headNum, int32_t kvHeadNum, float qkScale, ala_tensor* attnOut, ala_tensor* lse,
+    uint64_t* workspaceSize, ala_op** op) {
+  NvtxRange nvtx_range("ala_paged_attention_get_workspace_size");
+  PagedAttnArgs a{};
+  a.query = query;
+  a.query_stride = queryStride;
+  a.key = key;
+  a.value = value;
+  a.block_tables = blockTables;
+  a.seq_len = seqLen;
+  a.kv_seq_len = kvSeqLen;
+  a.slopes = slopes;
+  a.mask_type = maskType;
+  a.heads = headNum;
+  a.kv_heads = kvHeadNum;
+  a.qk_scale = qkScale;
+  a.out_scale = 1.f;
+  a.out = attnOut;
+  a.lse = lse;
+  return plan_paged(a, workspaceSize, op, "ala_paged_attention_get_workspace_size");
+}
+
+extern "C" int ala_paged_attention(void* workspace, uint64_t workspaceSize, ala_op* op, ala_stream_t stream) {
+  NvtxRange nvtx_range("ala_paged_attention");
+  return run_paged(workspace, workspaceSize, op, stream, ala_op::kPagedAttn, "ala_paged_attention");
+}
+
+extern "C" int ala_paged_diff_attention_get_workspace_size(
+    const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
+    const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* lambda,
+    const ala_tensor* normWeight, float normEps, float outScale, int maskType, int32_t headNum, int32_t kvHeadNum,
+    float qkScale, ala_tensor* attnOut, uint64_t* workspaceSize, ala_op** op) {
+  NvtxRange nvtx_range("ala_paged_diff_attention_get_workspace_size");
+  PagedAttnArgs a{};
+  a.query = query;
+  a.query_stride = queryStride;
+  a.key = key;
+  a.value = value;
+  a.block_tables = blockTables;
+  a.seq_len = seqLen;
+  a.kv_seq_len = kvSeqLen;
+  a.lambda = lambda;
+  a.norm_weight = normWeight;
+  a.norm_eps = normEps;
+  a.out_scale = outScale;
+  a.mask_type = maskType;
+  a.heads = headNum;
+  a.kv_heads = kvHeadNum;
+  a.qk_scale = qkScale;
+  a.out = attnOut;
+  a.diff = true;
+  return plan_paged(a, workspaceSize, op, "ala_paged_diff_attention_get_workspace_size");
+}
+
+extern "C" int ala_paged_diff_attention(void* workspace, uint64_t workspaceSize, ala_op* op, ala_stream_t stream) {
+  NvtxRange nvtx_range("ala_paged_diff_attention");
+  return run_paged(workspace, workspaceSize, op, stream, ala_op::kPagedDiff, "ala_paged_diff_attention");
 }

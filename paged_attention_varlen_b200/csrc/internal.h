@@ -30,7 +30,9 @@ enum DeviceStatus : int {
   kDevTimeoutPFull = 0x108,
   kDevTimeoutODone = 0x109,
   kDevTimeoutFinal = 0x10A,
-  kDevBadBlockIndex = 0x10B,  // ALA_DEBUG_BOUNDS builds: a block-table entry read lies outside [0, numBlocks)
+  kDevBadBlockIndex = 0x10B,  // a block-table entry read lies outside [0, numBlocks) (paged_attn.cu; elsewhere
+                              // ALA_DEBUG_BOUNDS builds only)
+  kDevBadLength = 0x10C,      // a device length was negative or past what its tensors hold, and was cut to it
 };
 
 #ifndef ALA_DEBUG_BOUNDS

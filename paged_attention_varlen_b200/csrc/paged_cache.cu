@@ -1,0 +1,262 @@
+// paged_cache.cu -- the bookkeeping of a serving step on the device: block tables, slot map, positions and
+// cumulative lengths from the requests' lengths (ala_paged_step), and the store of a step's new K / V rows
+// into the cache by slot (ala_paged_write).
+#include <algorithm>
+
+#include "../../include/ala.h"
+#include "paged.h"
+
+namespace ala {
+
+namespace {
+
+// ---------------------------------------------------------------------------------------------- step
+// With b the requests, n_b new tokens, c_b keys cached before (0 for a request that ended), s the block size:
+//   kv_b = c_b + n_b,  taken_b = ceil(kv_b / s) - ceil(c_b / s),  given_b = ceil(old c_b / s) if it ended
+// the blocks of ended requests go onto the stack in request order, new blocks come off its top in request
+// order, and token t of request b at position c_b + t has slot table[b][pos / s] * s + pos % s.
+//
+// Three exclusive sums over the batch are all it takes, so every CTA computes them for itself (one thread a
+// few rows) and keeps them in shared memory; the CTAs then share the rows and the tokens.  The one order
+// between them, pushes before pops and reads of the inputs before writes of outputs that may be the same
+// memory, is a cluster barrier, so a step is one launch.
+constexpr int kStepThreads = 1024;
+constexpr int kStepCluster = 8;
+
+struct StepRow {
+  int cu, taken, given, before;  // sums over earlier rows, and this row's keys cached before
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const PagedStepArgs a) {
+  extern __shared__ StepRow rows[];  // [batch + 1]
+  __shared__ int64_t warp_sum[3][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bs = a.block_size;
+  const int64_t room = (int64_t)a.max_blocks * bs;
+  const int per = (a.batch + kStepThreads - 1) / kStepThreads;
+  const int first = min(tid * per, a.batch), last = min(first + per, a.batch);
+  const int count = __ldg(a.free_count);
+  auto blocks_of = [&](int keys) { return (int)(((int64_t)keys + bs - 1) / bs); };
+
+  // ---- this thread's rows: their sums, and whether a length is out of range
+  int64_t sum[3] = {0, 0, 0};
+  bool bad = false;
+  for (int b = first; b < last; ++b) {
+    const int n = a.seq_len[b], ctx = a.context_len[b];
+    const bool ended = a.finished && a.finished[b] != 0;
+    const int64_t kv = (int64_t)n + (ended ? 0 : ctx);
+    if (n < 0 || ctx < 0 || ctx > room || kv > room) {
+      bad = true;
+      break;
+    }
+    sum[0] += n;
+    sum[1] += blocks_of((int)kv) - (ended ? 0 : blocks_of(ctx));
+    sum[2] += ended ? blocks_of(ctx) : 0;
+  }
+  int64_t x[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    x[i] = sum[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x[i], o);
+      if (lane >= o) x[i] += y;
+    }
+    if (lane == 31) warp_sum[i][warp] = x[i];
+  }
+  bad = __syncthreads_or(bad);
+  int64_t total[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int64_t mine = warp_sum[i][lane];
+    int64_t before = lane < warp ? mine : 0, all = mine;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    x[i] += before - sum[i];  // exclusive
+    total[i] = all;
+  }
+  const int code = bad                                                ? ALA_STEP_BAD_LENGTH
+                   : total[0] > a.n_tokens                            ? ALA_STEP_TOO_MANY_TOKENS
+                   : count < 0 || (int64_t)count + total[2] > a.capacity ? ALA_STEP_BAD_FREE_COUNT
+                   : total[1] > count + total[2]                      ? ALA_STEP_OUT_OF_BLOCKS
+                                                                      : 0;
+  if (code != 0) {  // the same for every CTA: the step changes nothing
+    cluster_sync();  // every CTA has read its inputs
+    const int t0 = blockIdx.x * kStepThreads + tid, stride = gridDim.x * kStepThreads;
+    for (int b = t0; b < a.batch; b += stride)
+      if (a.kv_seq_len != a.context_len) a.kv_seq_len[b] = a.context_len[b];
+    for (int b = t0; b <= a.batch; b += stride) a.cu_seq_len[b] = 0;
+    for (int t = t0; t < a.n_tokens; t += stride) {
+      a.slot_mapping[t] = -1;
+      a.positions[t] = 0;
+    }
+    if (t0 == 0) {
+      *a.free_count_out = count;
+      *a.status = code;
+    }
+    return;
+  }
+  {
+    int64_t cu = x[0], taken = x[1], given = x[2];
+    for (int b = first; b < last; ++b) {
+      const int n = a.seq_len[b], ctx = a.context_len[b];
+      const bool ended = a.finished && a.finished[b] != 0;
+      const int before = ended ? 0 : ctx;
+      rows[b] = StepRow{(int)cu, (int)taken, (int)given, before};
+      cu += n;
+      taken += blocks_of(before + n) - blocks_of(before);
+      given += ended ? blocks_of(ctx) : 0;
+    }
+    if (tid == 0) rows[a.batch] = StepRow{(int)total[0], (int)total[1], (int)total[2], 0};
+  }
+  __syncthreads();
+
+  // ---- blocks of ended requests onto the stack, one warp per row
+  const int warps = gridDim.x * (kStepThreads / 32), w0 = blockIdx.x * (kStepThreads / 32) + warp;
+  bool bad_block = false;
+  if (total[2] > 0) {
+    for (int b = w0; b < a.batch; b += warps) {
+      const int at = count + rows[b].given, n = rows[b + 1].given - rows[b].given;
+      const int32_t* row = a.block_tables + (int64_t)b * a.max_blocks;
+      for (int i = lane; i < n; i += 32) {
+        const int blk = row[i];
+        bad_block |= blk < 0 || blk >= a.capacity;
+        a.free_blocks[at + i] = blk;
+      }
+    }
+  }
+  // one thread clears the status before any CTA may report into it
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
+  cluster_sync();
+
+  // ---- new blocks off its top; what other CTAs pushed is read past L1
+  const int top = count + (int)total[2];
+  for (int b = w0; b < a.batch; b += warps) {
+    const StepRow r = rows[b];
+    const int n = rows[b + 1].taken - r.taken, have = blocks_of(r.before);
+    int32_t* row = a.block_tables + (int64_t)b * a.max_blocks;
+    for (int i = lane; i < n; i += 32) {
+      const int blk = __ldcg(a.free_blocks + (top - 1 - r.taken - i));
+      bad_block |= blk < 0 || blk >= a.capacity;
+      row[have + i] = blk;
+    }
+    if (lane == 0) {
+      a.kv_seq_len[b] = r.before + (rows[b + 1].cu - r.cu);
+      a.cu_seq_len[b] = r.cu;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.cu_seq_len[a.batch] = (int)total[0];
+    *a.free_count_out = top - (int)total[1];
+  }
+  // ---- slot and position of every token; a page that a row already had is in its table, a new one is still
+  // on the stack's top (nothing is written over it here)
+  for (int t = blockIdx.x * kStepThreads + tid; t < a.n_tokens; t += gridDim.x * kStepThreads) {
+    int slot = -1, pos = 0;
+    if (t < total[0]) {
+      int lo = 0, hi = a.batch;  // the last row with cu <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (rows[mid].cu <= t) lo = mid;
+        else hi = mid;
+      }
+      const StepRow r = rows[lo];
+      pos = r.before + t - r.cu;
+      const int page = pos / bs, have = blocks_of(r.before);
+      const int blk = page < have ? a.block_tables[(int64_t)lo * a.max_blocks + page]
+                                  : __ldcg(a.free_blocks + (top - 1 - r.taken - (page - have)));
+      if (blk >= 0 && blk < a.capacity) slot = blk * bs + pos - page * bs;
+      else bad_block = true;
+    }
+    a.slot_mapping[t] = slot;
+    a.positions[t] = pos;
+  }
+  if (bad_block) *a.status = ALA_STEP_BAD_BLOCK;
+}
+
+// ---------------------------------------------------------------------------------------------- write
+// Token t's K row goes to row slots[t] of the K cache and its V row to the same row of the V cache; slots
+// outside the cache (-1: padding) are skipped.  Nothing is computed: bytes bound it, so a thread has several
+// loads in flight before its first store.  `lanes` threads (a power of two) serve one token.
+template <typename V>
+__global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a, int lanes) {
+  constexpr int U = 4;
+  const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+  if (t >= a.n_tokens) return;
+  const int lane = threadIdx.x & (lanes - 1);
+  const int64_t slot = __ldg(a.slots + t);
+  if (slot < 0 || slot >= a.n_slots) return;
+  const int64_t nk = a.key_row / sizeof(V), nv = a.value_row / sizeof(V);
+  const V* ks = reinterpret_cast<const V*>(a.key + t * a.key_stride);
+  const V* vs = reinterpret_cast<const V*>(a.value + t * a.value_stride);
+  V* kd = reinterpret_cast<V*>(a.key_cache + slot * a.key_row);
+  V* vd = reinterpret_cast<V*>(a.value_cache + slot * a.value_row);
+  for (int64_t j0 = lane; j0 < nk + nv; j0 += (int64_t)lanes * U) {
+    V r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = j0 + (int64_t)u * lanes;
+      if (j < nk + nv) r[u] = j < nk ? ks[j] : vs[j - nk];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = j0 + (int64_t)u * lanes;
+      if (j < nk) kd[j] = r[u];
+      else if (j < nk + nv) vd[j - nk] = r[u];
+    }
+  }
+}
+
+template <typename V>
+cudaError_t write_as(const PagedWriteArgs& a, cudaStream_t stream) {
+  const int64_t n = (a.key_row + a.value_row) / (int64_t)sizeof(V);
+  int lanes = 1;
+  while (lanes < 256 && lanes * 4 < n) lanes *= 2;
+  const int64_t per_block = 256 / lanes;
+  paged_write_kernel<V><<<(unsigned)((a.n_tokens + per_block - 1) / per_block), 256, 0, stream>>>(a, lanes);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_step(const PagedStepArgs& a, cudaStream_t stream) {
+  const int smem = (int)sizeof(StepRow) * (a.batch + 1);
+  cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(StepRow) * (kPagedStepMaxBatch + 1));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int ctas = a.n_tokens > 2 * kStepThreads || a.batch > kStepThreads ? kStepCluster : 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kStepThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_step_kernel, a);
+}
+
+cudaError_t launch_paged_write(const PagedWriteArgs& a, cudaStream_t stream) {
+  if (a.n_tokens == 0 || a.n_slots == 0 || a.key_row + a.value_row == 0) return cudaSuccess;
+  // the widest access that every address, stride and row allows: 16-byte rows are the rule, the others serve
+  // odd row sizes and views
+  const uint64_t all = reinterpret_cast<uint64_t>(a.key) | reinterpret_cast<uint64_t>(a.value) |
+                       reinterpret_cast<uint64_t>(a.key_cache) | reinterpret_cast<uint64_t>(a.value_cache) |
+                       (uint64_t)a.key_stride | (uint64_t)a.value_stride | (uint64_t)a.key_row | (uint64_t)a.value_row;
+  if (all % 16 == 0) return write_as<uint4>(a, stream);
+  if (all % 4 == 0) return write_as<uint32_t>(a, stream);
+  return write_as<uint8_t>(a, stream);
+}
+
+}  // namespace ala

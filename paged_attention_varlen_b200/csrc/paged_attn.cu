@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr int KV_BYTES = TK * D * 2;
   static constexpr int NSK = D == 64 ? 6 : 3;
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
-  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 2 + 2 + 1 + 1;
+  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int SMEM = 1024 + Q_BYTES + (NSK + NSV) * KV_BYTES + 128 * 8 + N_BARS * 8 + 64;
   static constexpr uint32_t IDESC_QK = instr_desc(ElemFmt<T>::fmt, false, false, 128, TK);
   static constexpr uint32_t IDESC_PV = instr_desc(ElemFmt<T>::fmt, false, true, 128, D);
@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = v_empty + NSV;  // [2] per S buffer
   uint64_t* p_full = s_full + 2;     // [2]
   uint64_t* pv_done = p_full + 2;
-  uint64_t* fin = pv_done + 1;
+  uint64_t* o_done = pv_done + 1;  // the item's last product
+  uint64_t* join = o_done + 1;     // meetings of the softmax warps, with the limit of every other wait
+  uint64_t* fin = join + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   __shared__ Start st;
   __shared__ int64_t red[2 * kThreads / 32 + 2];
@@ -525,6 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + s, 128);
     }
     mbar_init(pv_done, 1);
+    mbar_init(o_done, 1);
+    mbar_init(join, 128);
     mbar_init(fin, 1);
     fence_mbar_init();
   }
@@ -661,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(v_empty + slot);
         commit(pv_done);
+        if (i == cnt - 1) commit(o_done);
         if (i + 2 < cnt) ok = wait_all(pv_done, g & 1, kDevTimeoutODone) && issue_qk(g + 2);
       }
       g0 += cnt;
@@ -675,9 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_col = tmem + lane_base + C::O_COL;
     const int group = p.group;
-    uint32_t g = 0;
+    uint32_t g = 0, item = 0, meetings = 0;
     bool ok = true, owner = false;
     int64_t line = st.line;
+    auto meet = [&]() {
+      mbar_arrive(join);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(join, meetings & 1, status, kDevTimeoutODone));
+      ++meetings;
+    };
     do {
       const int rows = w.rows(p);
       const bool quarters = rows <= 32;       // rows repeated in each lane quarter, which shares the keys
@@ -752,16 +762,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full + (g & 1));
       }
       if (!ok) break;
-      // the last two products in turn: S of the last tile says only that the product two before it is done, and a
-      // wait for a phase passes while the barrier is still one phase short of it
-      if (cnt > 1) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 2) & 1, status, kDevTimeoutODone));
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, status, kDevTimeoutODone));
+      // o_done has one phase per item and is waited for once in each, so no wait can meet the phase before or
+      // after its own (pv_done may be two phases on, or one short, when a warp gets here)
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done, item & 1, status, kDevTimeoutODone));
+      ++item;
       if (!ok) break;
       tc_fence_after();
       // ---- join the four lane quarters into the first: O' = sum_w 2^(m_w - M) O_w, l alike
       if (quarters) {
         sML[warp * 32 + lane] = make_float2(rs.m, rs.l);
-        named_barrier_sync(1, 128);
+        meet();
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) top = fmaxf(top, sML[q * 32 + lane].x);
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          named_barrier_sync(1, 128);
+          meet();
           if (warp == 0) {
 #pragma unroll 1
             for (int c32 = 0; c32 < D / 64; ++c32) {
@@ -823,9 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-          named_barrier_sync(1, 128);
+          meet();
         }
       }
+      if (!ok) break;
       // ---- epilogue
       const bool whole = w.t0 == 0 && w.t1 == w.n;
       const bool has_rows = warp_rows && (!quarters || warp == 0);

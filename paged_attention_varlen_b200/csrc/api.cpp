@@ -94,7 +94,7 @@ CUtensorMapDataType tma_dtype(int32_t dtype) {
 
 namespace ala {
 bool encode_rows_heads_d(CUtensorMap* map, void* base, int32_t dtype, int64_t rows, int64_t heads, int64_t d,
-                         int box_rows, bool mn_major_operand) {
+                         int box_rows, bool mn_major_operand, int l2_promotion) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return false;
   const int es = elem_size(dtype);
@@ -105,7 +105,10 @@ bool encode_rows_heads_d(CUtensorMap* map, void* base, int32_t dtype, int64_t ro
   const CUtensorMapSwizzle sw =
       (mn_major_operand && es == 4) ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B;
   return enc(map, tma_dtype(dtype), 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             l2_promotion == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+             : l2_promotion == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                   : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace ala
 

@@ -183,9 +183,10 @@ inline int64_t prefill_unit_count(int32_t batch, const int32_t* seq_len, int32_t
 inline int64_t prefill_unit_cost(const PrefillUnit& u) { return (int64_t)u.n_tiles[0] + u.n_tiles[1] + 1; }
 
 // Tensor map over a [rows, heads, d] tensor (d innermost): box of 128 bytes of d, one head and
-// `box_rows` rows, 128-byte swizzle (32-byte atoms for a 32-bit MN-major operand).  Defined in api.cpp.
+// `box_rows` rows, 128-byte swizzle (32-byte atoms for a 32-bit MN-major operand); l2_promotion: bytes that L2
+// fetches around what a box touches (256, 128 or 0: nothing more).  Defined in api.cpp.
 bool encode_rows_heads_d(CUtensorMap* map, void* base, int32_t dtype, int64_t rows, int64_t heads, int64_t d,
-                         int box_rows, bool mn_major_operand);
+                         int box_rows, bool mn_major_operand, int l2_promotion = 256);
 
 // dtype codes as in include/ala.h
 enum : int32_t { kF16 = 0, kBF16 = 1, kF32 = 2, kI32 = 3 };

@@ -5,28 +5,36 @@
 //   O[t, h] = sum_j (softmax_j(s1) - lambda_h softmax_j(s2)) v_j, s_m = qkScale q[t, 2h + m] . k_(m),j
 //             and then, optionally, O <- O * rsqrt(mean(O^2) + eps) * w               (ala_paged_diff_attention)
 //
-// Rows.  The queries of one kv head are packed (token, head of the group) into tiles of up to 128 rows, so a
-// single token of a group of 8 heads is one tile of 8 rows and K / V are read once for the group.
+// Rows.  The queries of one kv head are packed (token, head of the group), so that K / V are read once for the
+// group.  An item is the rows of up to two blocks of 128 (one at D = 256, whose O leaves no room in tensor
+// memory for a second) against one kv head's keys, in tiles of 128 keys (64 at D = 256).
+//   two blocks    more than 128 rows: every tile serves both blocks, and one block's products run while the
+//                 other's softmax does
+//   alternating   up to 128 rows: the blocks are the same rows, and take the tiles in turn; joined at the end
+//   quarters      up to 32 rows, alternating too: the rows are repeated in the four lane quarters of a block,
+//                 quarter w takes a quarter of each tile's keys (P is zero on the others), so that all the
+//                 softmax warps share the exponentials of a single token.  With 16 rows or fewer, the upper
+//                 lanes of a quarter carry what rounding P to 16 bits dropped: P V is then exact to 2^-17 or
+//                 so and costs no further product.
 //
 // Differential attention is the same kernel over K rows [k1 | k2] of 2d elements, as they lie in the cache:
-// the query row of map 1 is [q1 | 0], that of map 2 is [0 | q2], and the two maps of a head are neighbouring
-// rows, so that their difference is one shuffle between neighbouring lanes.  Decoding reads the cache once
-// and pays nothing for the zeros; a compute-bound chunk pays 8d instead of 6d products per pair.
+// the query row of map 1 is [q1 | 0], that of map 2 is [0 | q2].  With two blocks a block is a map, and its
+// score product runs over that map's half alone; otherwise the two maps of a head are neighbouring rows, and
+// the zeros cost a decoding step nothing, since it is bound by the bytes of the cache.
 //
 // Work split.  All key tiles of all (sequence, kv head, row tile) items form one line; CTA c of G takes the
 // tiles [c T / G, (c + 1) T / G).  A CTA finds its start by a scan over the batch and a search inside one
 // sequence, so the schedule needs no host lengths and no planning launch, and every CTA gets the same number
 // of tiles whatever the lengths are.  An item cut by a CTA boundary leaves unnormalised fp32 partials with
 // the running max and sum of each row; paged_combine_kernel joins them in segment order.
+// Tiles run from the last key to the first: under ALiBi the largest scores come first, so that the running
+// max hardly moves after the first tile and O is not rescaled (first to last rescaled it at every tile).
 //
-// Pipeline of a CTA (one per SM):
-//   warps 4, 5  TMA producers of the K and the V ring; lane i gathers box i of a tile through the block table
-//   warp 6      tcgen05 issuer: S = Q K^T into one of two TMEM buffers, O += P V with P read from TMEM;
-//               QK of tile j + 1 runs while the softmax works on tile j
-//   warps 0..3  softmax, thread r owns row r (TMEM lane r).  With 32 rows or fewer, the rows are repeated in
-//               the four lane quarters and quarter w takes a quarter of each tile's keys (P is zero on the
-//               others), so that all four warps share the exponentials of a single token; the quarters are
-//               joined through shared memory at the end of the item.
+// Pipeline of a CTA (one per SM), NB blocks:
+//   warps 0 .. 4 NB - 1   softmax of block b, thread r owns row r (TMEM lane r)
+//   then a warp each      TMA producer of the K ring, of the V ring (lane i gathers box i of a tile through
+//                         the block table), and the tcgen05 issuer: S_b = Q K^T, O_b += P_b V with P_b read
+//                         from TMEM over S_b, P V in two halves of the keys
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,16 +54,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
 constexpr int kGrid = 148;                 // one CTA per SM of a B200
-constexpr int kThreads = 256;
 constexpr int kCombineY = 4;               // blocks per segment list in the combine grid
 
 // What a split item's first CTA leaves for the combine kernel.
 struct PagedDesc {
   int32_t n_seg;    // CTAs that hold a segment of the item (0: this CTA starts no split item)
   int32_t token0;   // first token of the row tile
-  int32_t rows;     // valid rows
+  int32_t tokens;   // its tokens
   int32_t kv_head;
   int32_t pos0;     // absolute position of token0
+  int32_t two;      // rows in two blocks
 };
 
 struct PagedParams {
@@ -66,16 +74,26 @@ struct PagedParams {
   float* lse;
   int* status;
   PagedDesc* desc;  // [kGrid]
-  float2* ml;       // [kGrid][2][128]: running max (log2 units) and sum of each partial row
-  float* part;      // [kGrid][2][128][D]
+  float2* ml;       // [kGrid][2][128 NB]: running max (log2 units) and sum of each partial row
+  float* part;      // [kGrid][2][128 NB][D]
   int64_t q_stride;
   int32_t n_tokens, batch, max_blocks, block_size, num_blocks, mask_type;
   int32_t heads, group, kv_heads;  // query heads, per kv head (both maps counted)
-  int32_t tb;                      // tokens per row tile: 128 / group
+  int32_t tb1, tb;                 // tokens of one block of rows (128 / group), tokens per row tile
   int32_t dq, row;                 // query head size, elements of a K / V row
   int32_t box_rows;
   float scale_log2, norm_eps, out_scale;
+
+  __host__ __device__ int maps() const { return dq == row ? 1 : 2; }
 };
+
+// Row of an item's partials that holds (token of the tile, head of the group without its map, map).
+__device__ __forceinline__ int partial_row(const PagedParams& p, bool two, int token, int hh, int map) {
+  const int maps = p.maps();
+  if (!two) return token * p.group + hh * maps + map;
+  if (maps == 2) return map * 128 + token * (p.group / 2) + hh;
+  return token < p.tb1 ? token * p.group + hh : 128 + (token - p.tb1) * p.group + hh;
+}
 
 template <typename T>
 struct ElemFmt;
@@ -88,26 +106,29 @@ struct ElemFmt<__nv_bfloat16> {
   static constexpr uint32_t fmt = 1;
 };
 
-// Two S buffers of TK columns and O of D columns fit tensor memory for D up to 256 with 64-key tiles.  The
-// rings fill what shared memory leaves: a tile arrives a few thousand cycles after its load is issued, so
+// The rings fill what shared memory leaves: a tile arrives a few thousand cycles after its load is issued, so
 // depth is what keeps HBM busy.
-template <typename T, int D_>
+// NQ: blocks of Q rows.  With one (items of at most 128 rows), the second's room goes to the rings.
+template <typename T, int D_, int NQ_>
 struct Cfg {
-  static constexpr int D = D_;
+  static constexpr int D = D_, NQ = NQ_;
+  static constexpr int NB = D == 256 ? 1 : 2;     // blocks of 128 rows
   static constexpr int TK = D == 256 ? 64 : 128;  // keys per tile
+  static constexpr int THREADS = NB * 128 + 128;
   static constexpr int CB = D / 64;               // 128-byte column blocks of a row
-  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int Q_BYTES = 128 * D * 2;     // one block
   static constexpr int KV_BYTES = TK * D * 2;
-  static constexpr int NSK = D == 64 ? 6 : 3;
+  static constexpr int NSK = D == 64 ? 5 : D == 128 ? 4 - NQ : 3;
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
-  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 2 + 2 + 1 + 1 + 1 + 1;
-  static constexpr int SMEM = 1024 + Q_BYTES + (NSK + NSV) * KV_BYTES + 128 * 8 + N_BARS * 8 + 64;
-  static constexpr uint32_t IDESC_QK = instr_desc(ElemFmt<T>::fmt, false, false, 128, TK);
-  static constexpr uint32_t IDESC_PV = instr_desc(ElemFmt<T>::fmt, false, true, 128, D);
-  static constexpr uint32_t O_COL = 2 * TK;  // S0 [0, TK) S1 [TK, 2 TK) O [2 TK, 2 TK + D)
+  static constexpr int SCRATCH = NQ * Q_BYTES;    // the Q buffers between items: what the joins pass through
+  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 4 * 2 + 2 + 1;
+  static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;
+  static constexpr uint32_t S_COL(int b) { return b * TK; }
+  static constexpr uint32_t O_COL(int b) { return 2 * TK + (NB == 2 ? b * D : 0); }
   static constexpr uint32_t TMEM_COLS = 512;
-  static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(O_COL + D <= TMEM_COLS, "tensor memory budget");
+  static_assert(SMEM + 512 <= 232448, "shared memory budget (512: the static part)");
+  static_assert(SCRATCH / (NB * 4 * 32 * 4) % 32 == 0, "the joins take 32 columns at a time");
+  static_assert(2 * TK + NB * D <= TMEM_COLS, "tensor memory budget");
 };
 
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* a) {
@@ -127,6 +148,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half*) {
   __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+
+__device__ __forceinline__ float2 unpack2(uint32_t v, __nv_bfloat16*) {
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v, __half*) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 
 // ---------------------------------------------------------------------------------------------- the work line
 
@@ -229,7 +255,7 @@ struct Walker {
     enter(p);
     return true;
   }
-  __device__ __forceinline__ int rows(const PagedParams& p) const { return min(p.tb, s.seq - rt * p.tb) * p.group; }
+  __device__ __forceinline__ int tokens(const PagedParams& p) const { return min(p.tb, s.seq - rt * p.tb); }
 };
 
 struct Start {
@@ -239,8 +265,8 @@ struct Start {
 };
 
 // Every thread of the CTA scans the batch (kThreads sequences at a time); the results are in *st after the
-// caller's __syncthreads.  `red` holds 2 * kThreads / 32 + 2 words.
-template <int TK>
+// caller's __syncthreads.  `red` holds 2 * kThreads / 32 words.
+template <int TK, int kThreads>
 __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = kThreads / 32;
@@ -395,16 +421,18 @@ struct RowState {
   float slope_log2;
 };
 
-// One tile's softmax for the NC columns from `c0` of a row: P over S in TMEM, returns the factor that O must
-// be rescaled by (1: none).
-template <typename T, int NC>
-__device__ __forceinline__ float softmax_cols(const PagedParams& p, RowState& rs, uint32_t s_col, int j0, int c0) {
-  float x[NC];
-  load_cols<NC>(s_col + c0, x);
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Scores of the NC columns from key `first` of a row, in log2 units (raw where raw_max says so); returns their
+// maximum in log2 units.
+template <int NC>
+__device__ __forceinline__ float scores(const PagedParams& p, const RowState& rs, float (&x)[NC], int first, bool raw_max) {
   const int mt = p.mask_type;
   const float scale = p.scale_log2;
-  const bool raw_max = (mt == 0 || mt == 9) && scale > 0.f;  // max of the raw scores, scale folded into the exponent
-  const int first = j0 + c0;
   const int lim = rs.last_key - first;  // columns c <= lim are allowed
   if (mt == 3 || mt == 5) {
     // right- and left-aligned bias differ by a per-row constant; both use (j - pos)
@@ -412,9 +440,10 @@ __device__ __forceinline__ float softmax_cols(const PagedParams& p, RowState& rs
 #pragma unroll
     for (int c = 0; c < NC; ++c) x[c] = fmaf(x[c], scale, fmaf(rs.slope_log2, static_cast<float>(c), b0));
   } else if (mt == 4) {
+    const float d0 = static_cast<float>(rs.pos - first);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      x[c] = fmaf(x[c], scale, -rs.slope_log2 * sqrtf(fmaxf(static_cast<float>(rs.pos - first - c), 0.f)));
+      x[c] = fmaf(x[c], scale, -rs.slope_log2 * sqrt_approx(fmaxf(d0 - static_cast<float>(c), 0.f)));
   } else if (!raw_max) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) x[c] *= scale;
@@ -431,35 +460,46 @@ __device__ __forceinline__ float softmax_cols(const PagedParams& p, RowState& rs
     mx2 = max3(mx2, x[c + 4], x[c + 5]);
     mx3 = max3(mx3, x[c + 6], x[c + 7]);
   }
-  float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-  if (raw_max) mx *= scale;
+  const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+  return raw_max ? mx * scale : mx;
+}
+
+// Takes a tile's maximum into the running one.  Returns the factor that O and l must be rescaled by (1: none).
+__device__ __forceinline__ float grow(RowState& rs, float mx) {
   const float m_new = fmaxf(rs.m, mx);
-  float alpha = 1.f;
-  if (m_new - rs.m > kRescaleThreshold) {  // false while both are -inf
-    alpha = fast_exp2(rs.m - m_new);
-    rs.m = m_new;
-  }
-  const float m_base = (rs.m == -INFINITY) ? 0.f : rs.m;
-  const uint64_t scale2 = f2pack(raw_max ? scale : 1.f, raw_max ? scale : 1.f);
-  const uint64_t negm2 = f2pack(-m_base, -m_base);
-  uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-  // P is rounded to the operand type of the tensor core; the sum takes the unrounded values, so a row's
-  // rounding errors (at most half a step of each weight) average out instead of biasing the normalisation
-  uint32_t pk[NC / 2];
+  if (!(m_new - rs.m > kRescaleThreshold)) return 1.f;  // so while both are -inf
+  const float alpha = fast_exp2(rs.m - m_new);
+  rs.m = m_new;
+  return alpha;
+}
+
+// P = 2^(x - m) of N columns, packed; adds to the four partial sums.  P is rounded to the operand
+// type of the tensor core; the sum takes the unrounded values, so a row's rounding errors (at most half a step
+// of each weight) average out instead of biasing the normalisation.  `rest`: the part that rounding drops.
+template <typename T, int N>
+__device__ __forceinline__ void exponentials(const float (&x)[N], uint64_t scale2, uint64_t negm2, uint64_t (&acc)[4],
+                                             uint32_t (&pk)[N / 2], bool rest) {
 #pragma unroll
-  for (int c = 0; c < NC; c += 2) {
+  for (int c = 0; c < N; c += 2) {
     float e0, e1;
     f2unpack(fma_x2(f2pack(x[c], x[c + 1]), scale2, negm2), e0, e1);
     e0 = fast_exp2(e0);
     e1 = fast_exp2(e1);
     acc[(c >> 1) & 3] = add_x2(acc[(c >> 1) & 3], f2pack(e0, e1));
     pk[c / 2] = pack2(e0, e1, (T*)nullptr);
+    if constexpr (N <= 32) {
+      if (rest) {
+        const float2 r = unpack2(pk[c / 2], (T*)nullptr);
+        pk[c / 2] = pack2(e0 - r.x, e1 - r.y, (T*)nullptr);
+      }
+    }
   }
-  store_p<NC / 2>(s_col + c0 / 2, pk);
+}
+
+__device__ __forceinline__ float sum4(const uint64_t (&acc)[4]) {
   float s0, s1;
   f2unpack(add_x2(add_x2(acc[0], acc[1]), add_x2(acc[2], acc[3])), s0, s1);
-  rs.l = rs.l * alpha + (s0 + s1);
-  return alpha;
+  return s0 + s1;
 }
 
 // O rows in TMEM times alpha.
@@ -479,41 +519,42 @@ __device__ __forceinline__ void scale_rows(uint32_t o_col, float alpha) {
 
 // ---------------------------------------------------------------------------------------------- kernel
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p) {
-  using C = Cfg<T, D>;
-  constexpr int TK = C::TK, NSK = C::NSK, NSV = C::NSV;
+  using C = Cfg<T, D, NQ>;
+  constexpr int TK = C::TK, NSK = C::NSK, NSV = C::NSV, NB = C::NB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                     // [Q_BYTES]; between items the scratch of the join of lane quarters
-  uint8_t* sK = sQ + C::Q_BYTES;          // [NSK][KV_BYTES]
-  uint8_t* sV = sK + NSK * C::KV_BYTES;   // [NSV][KV_BYTES]
-  float2* sML = reinterpret_cast<float2*>(sV + NSV * C::KV_BYTES);  // [4][32]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sML + 128);
+  uint8_t* sQ = smem;                        // [NQ][Q_BYTES]; between items the scratch of the joins
+  uint8_t* sK = sQ + NQ * C::Q_BYTES;        // [NSK][KV_BYTES]
+  uint8_t* sV = sK + NSK * C::KV_BYTES;      // [NSV][KV_BYTES]
+  float* sM = reinterpret_cast<float*>(sV + NSV * C::KV_BYTES);  // [256] maxima and sums of the joins
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sM + 256);
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 1;
   uint64_t* k_empty = k_full + NSK;
   uint64_t* v_full = k_empty + NSK;
   uint64_t* v_empty = v_full + NSV;
   uint64_t* s_full = v_empty + NSV;  // [2] per S buffer
-  uint64_t* p_full = s_full + 2;     // [2]
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* o_done = pv_done + 1;  // the item's last product
-  uint64_t* join = o_done + 1;     // meetings of the softmax warps, with the limit of every other wait
-  uint64_t* fin = join + 1;
+  uint64_t* p_lo = s_full + 2;       // [2] P of the tile's first half of keys written
+  uint64_t* p_full = p_lo + 2;       // [2] all of P
+  uint64_t* pv_done = p_full + 2;    // [2]
+  uint64_t* o_done = pv_done + 2;    // [2] per block: the item's last product
+  uint64_t* fin = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   __shared__ Start st;
-  __shared__ int64_t red[2 * kThreads / 32 + 2];
+  __shared__ int64_t red[2 * C::THREADS / 32];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   int* status = p.status;
+  constexpr int kWarpK = NB * 4, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 
-  find_start<TK>(p, &st, red);
+  find_start<TK, C::THREADS>(p, &st, red);
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 128);
+    mbar_init(q_full, NB * 128);
     for (int s = 0; s < NSK; ++s) {
       mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
@@ -524,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full + s, 1);
+      mbar_init(p_lo + s, 128);
       mbar_init(p_full + s, 128);
+      mbar_init(pv_done + s, 1);
+      mbar_init(o_done + s, 1);
     }
-    mbar_init(pv_done, 1);
-    mbar_init(o_done, 1);
-    mbar_init(join, 128);
     mbar_init(fin, 1);
     fence_mbar_init();
   }
@@ -537,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) p.desc[blockIdx.x].n_seg = 0;
     return;
   }
-  if (warp == 6) {
+  if (warp == kWarpMma) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -557,11 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.s = load_seq(p, w.b, w.cu, w.raw);
   w.enter(p);
 
-  // Barrier phases run on across items: the rings and the S buffers by counters of all tiles (slot g % depth,
-  // phase g / depth), q_full by the item.
-  if (warp == 4 || warp == 5) {
-    // -------------------------------------------------------------- producers: warp 4 K, warp 5 V
-    const bool is_k = warp == 4;
+  // An item of cnt tiles is U steps: step u fills S buffer u & 1 and multiplies its P.  With two blocks of rows,
+  // steps 2i and 2i + 1 are tile i for block 0 and 1; otherwise step u is tile u, for block u & 1 of the two that
+  // hold the same rows (NB = 1: for the one block).  Ring phases run on across items by a counter of tiles (slot
+  // g % depth, phase g / depth), those of a buffer by its count of steps, q_full and o_done by items.
+  auto is_two = [&]() { return NQ == 2 && w.tokens(p) * p.group > 128; };
+  // register split for NB = 2: the softmax warps take 216 each, the others keep 72 (256 * 216 + 128 * 72 =
+  // 64512 = 384 * 168, all that the block is launched with)
+  if (warp >= kWarpK) {
+    if constexpr (NB == 2) regs_decrease<72>();
+  }
+  if (warp == kWarpK || warp == kWarpV) {
+    // -------------------------------------------------------------- producers
+    const bool is_k = warp == kWarpK;
     const int depth = is_k ? NSK : NSV;
     uint8_t* ring = is_k ? sK : sV;
     uint64_t* full_bar = is_k ? k_full : v_full;
@@ -578,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* bt = p.block_tables + (size_t)w.b * p.max_blocks;
       const int pages = (w.s.kv + bs - 1) / bs;
       // the table entry of a tile's box is fetched one tile ahead, so its latency is not in the loop
-      int pg = (w.t0 * TK + lane * box) / bs;
+      int pg = ((w.t1 - 1) * TK + lane * box) / bs;
       int blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
-      for (int j = w.t0; j < w.t1; ++j, ++g) {
+      for (int j = w.t1 - 1; j >= w.t0; --j, ++g) {
         const int slot = g % depth;
         const int pos = j * TK + lane * box;
         int row = oob_row;  // past the last page: the load fills zeros
@@ -588,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (blk >= 0 && blk < p.num_blocks) row = blk * bs + (pos - pg * bs);
           else atomicCAS(status + 1, 0, kDevBadBlockIndex);
         }
-        if (j + 1 < w.t1) {
-          pg = (pos + TK) / bs;
+        if (j > w.t0) {
+          pg = (pos - TK) / bs;
           blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
         }
         if (g >= (uint32_t)depth &&
@@ -605,142 +654,172 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int cb = 0; cb < C::CB; ++cb) tma_load_3d(dst + cb * TK * 128, map, full_bar + slot, cb * 64, w.h, row);
         }
+        __syncwarp();
       }
     } while (ok && w.next(p));
     // never leave the CTA while loads this warp issued are still landing in shared memory
     for (uint32_t i = g >= (uint32_t)depth ? g - depth : 0; i < g; ++i)
       mbar_wait(full_bar + (i % depth), (i / depth) & 1, status, is_k ? kDevTimeoutKFull : kDevTimeoutVFull);
-  } else if (warp == 6) {
+    __syncwarp();
+  } else if (warp == kWarpMma) {
     // -------------------------------------------------------------- MMA issuer
     const bool leader = elect_one();
     const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_addr(sV), TK * 128, 1024);  // MN-major
-    constexpr uint64_t kStep = C::KV_BYTES >> 4;
+    constexpr uint64_t kQStep = C::Q_BYTES >> 4, kStep = C::KV_BYTES >> 4;
+    constexpr uint32_t kIdescQk = instr_desc(ElemFmt<T>::fmt, false, false, 128, TK);
+    // P V makes the row's columns only, rounded up to the instruction's step of 16
+    const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, false, true, 128, (p.row + 15) & ~15);
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
     };
     auto commit = [&](uint64_t* bar) {
       if (leader) mma_commit(bar);
     };
-    auto issue_qk = [&](uint32_t g) -> bool {
-      const int slot = g % NSK;
-      if (!wait_all(k_full + slot, (g / NSK) & 1, kDevTimeoutKFull)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t b0 = dk + slot * kStep;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int ke = kk * 16;
-          const uint64_t in = (uint64_t)(ke % 64) * 2;
-          mma_ss(tmem + (g & 1) * TK, dq + (((ke / 64) * (128 * 128) + in) >> 4), b0 + (((ke / 64) * (TK * 128) + in) >> 4),
-                 C::IDESC_QK, kk > 0, false);
-        }
-      }
-      commit(s_full + (g & 1));
-      commit(k_empty + slot);
-      return true;
-    };
     bool ok = true;
-    uint32_t g0 = 0, item = 0;
+    uint32_t g0 = 0, item = 0, sp0 = 0, sp1 = 0;
     do {
       const int cnt = w.t1 - w.t0;
-      // Q is written after the previous item's last P V, so both S buffers and O are free from here on
-      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(g0) && (cnt < 2 || issue_qk(g0 + 1));
-      for (int i = 0; i < cnt && ok; ++i) {
-        const uint32_t g = g0 + i;
-        const int slot = g % NSV;
-        if (!wait_all(v_full + slot, (g / NSV) & 1, kDevTimeoutVFull) ||
-            !wait_all(p_full + (g & 1), (g >> 1) & 1, kDevTimeoutPFull)) {
-          ok = false;
-          break;
-        }
+      const bool two = is_two();
+      const int U = two ? 2 * cnt : cnt;
+      auto issue_qk = [&](int u) -> bool {
+        const int b = u & 1;
+        const uint32_t g = g0 + (two ? u >> 1 : u);
+        const int slot = g % NSK;
+        if ((!two || b == 0) && !wait_all(k_full + slot, (g / NSK) & 1, kDevTimeoutKFull)) return false;
+        // the buffer's previous P has been multiplied (before the item: q_full says so)
+        if (u >= 2 && !wait_all(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, kDevTimeoutODone)) return false;
         tc_fence_after();
         if (leader) {
-          const uint64_t v0 = dv + slot * kStep;
-#pragma unroll
-          for (int kk = 0; kk < TK / 16; ++kk)
-            mma_ts(tmem + C::O_COL, tmem + (g & 1) * TK + kk * 8, v0 + ((kk * 16 * 128) >> 4), C::IDESC_PV,
-                   (i > 0 || kk > 0) ? 1u : 0u, false);
+          // the columns that hold q: a row's, or its map's where a block is a map
+          const int lo = two && p.maps() == 2 ? b * p.dq / 16 : 0;
+          const int hi = (two && p.maps() == 2 ? (b + 1) * p.dq + 15 : p.row + 15) / 16;
+          const uint64_t a0 = dq + (two ? b * kQStep : 0), b0 = dk + slot * kStep;
+          for (int kk = lo; kk < hi; ++kk) {
+            const uint64_t in = (uint64_t)(kk % 4) * 32;
+            mma_ss(tmem + C::S_COL(b), a0 + (((kk / 4) * (128 * 128) + in) >> 4), b0 + (((kk / 4) * (TK * 128) + in) >> 4),
+                   kIdescQk, kk > lo, false);
+          }
         }
-        commit(v_empty + slot);
-        commit(pv_done);
-        if (i == cnt - 1) commit(o_done);
-        if (i + 2 < cnt) ok = wait_all(pv_done, g & 1, kDevTimeoutODone) && issue_qk(g + 2);
+        commit(s_full + b);
+        if (!two || b == 1) commit(k_empty + slot);
+        return true;
+      };
+      // Q is written after the previous item's last product, so the S buffers and O are free from here on
+      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
+      for (int u = 0; u < U && ok; ++u) {
+        const int b = u & 1;
+        const uint32_t g = g0 + (two ? u >> 1 : u), ph = (b ? sp1 : sp0) + (u >> 1);
+        const int slot = g % NSV;
+        const uint64_t v0 = dv + slot * kStep;
+        auto issue_pv = [&](int half) {
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = half * (TK / 32); kk < (half + 1) * (TK / 32); ++kk)
+              mma_ts(tmem + C::O_COL(b), tmem + C::S_COL(b) + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv,
+                     (u >= NB || kk > 0) ? 1u : 0u, false);
+          }
+        };
+        ok = (two && b == 1) || wait_all(v_full + slot, (g / NSV) & 1, kDevTimeoutVFull);
+        if (!ok || !(ok = wait_all(p_lo + b, ph & 1, kDevTimeoutPFull))) break;
+        issue_pv(0);
+        if (!(ok = wait_all(p_full + b, ph & 1, kDevTimeoutPFull))) break;
+        issue_pv(1);
+        if (!two || b == 1) commit(v_empty + slot);
+        commit(pv_done + b);
+        if (u + NB >= U) commit(o_done + (NB == 2 ? b : 0));
+        if (u + 2 < U) ok = issue_qk(u + 2);
       }
       g0 += cnt;
+      sp0 += (U + 1) >> 1;
+      sp1 += U >> 1;
       ++item;
     } while (ok && w.next(p));
     // all tensor-core work this thread issued has finished before TMEM is released
     commit(fin);
     wait_all(fin, 0, kDevTimeoutFinal);
-  } else if (warp < 4) {
+  } else if (warp < kWarpK) {
     // -------------------------------------------------------------- softmax and epilogue
-    const int r = threadIdx.x;  // TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_col = tmem + lane_base + C::O_COL;
-    const int group = p.group;
-    uint32_t g = 0, item = 0, meetings = 0;
-    bool ok = true, owner = false;
+    if constexpr (NB == 2) regs_increase<216>();
+    const int blk = warp >> 2, wq = warp & 3;
+    const int r = threadIdx.x & 127;  // TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t o_col = tmem + lanes + C::O_COL(blk);
+    const int group = p.group, maps = p.maps(), gh = group / maps;
+    const bool raw_max = (p.mask_type == 0 || p.mask_type == 9) && p.scale_log2 > 0.f;  // scale folded into the exponent
+    const uint64_t scale2 = raw_max ? f2pack(p.scale_log2, p.scale_log2) : f2pack(1.f, 1.f);
+    uint32_t g0 = 0, sp0 = 0, sp1 = 0, items = 0;  // tiles, steps of the S buffers, items that this block took part in
+    bool owner = false;
+    // After a failed wait a warp skips what is left of the tiles, but goes on through the items, so that the
+    // warps meet as often as ever.
+    bool ok = true;
     int64_t line = st.line;
-    auto meet = [&]() {
-      mbar_arrive(join);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(join, meetings & 1, status, kDevTimeoutODone));
-      ++meetings;
-    };
+    auto meet = [&]() { named_barrier_sync(1, NB * 128); };
     do {
-      const int rows = w.rows(p);
-      const bool quarters = rows <= 32;       // rows repeated in each lane quarter, which shares the keys
-      const int rr = quarters ? lane : r;     // this thread's row of the tile
-      const bool valid = rr < rows;
-      const int tok = w.rt * p.tb + rr / group, head = w.h * group + rr % group;
-      const int64_t token = w.cu + tok;
+      const int cnt = w.t1 - w.t0, tokens = w.tokens(p);
+      const bool two = is_two();
+      const int steps = NB == 1 || two ? cnt : (cnt + 1 - blk) >> 1;  // this block's
+      const bool quarters = !two && tokens * group <= 32;
+      const bool carry = quarters && tokens * group <= 16;  // lanes 16..31 hold what rounding P drops
       const int off = w.s.kv - w.s.seq;
+      // this thread's row: its token in the tile and query head
+      int tok, qh;
+      bool valid;
+      if (two && maps == 2) {
+        tok = r / gh;
+        qh = (w.h * gh + r % gh) * 2 + blk;
+        valid = tok < tokens;
+      } else {
+        const int rr = quarters ? (carry ? lane & 15 : lane) : r;
+        tok = rr / group + (two ? blk * p.tb1 : 0);
+        qh = w.h * group + rr % group;
+        valid = tok < tokens && (!two || blk == 1 || rr / group < p.tb1);
+      }
+      const int64_t token0 = w.cu + (int64_t)w.rt * p.tb, token = token0 + tok;
       RowState rs;
       rs.m = -INFINITY;
       rs.l = 0.f;
-      rs.pos = tok + off;
+      rs.pos = w.rt * p.tb + tok + off;
       rs.last_key = !valid ? -1 : p.mask_type == 0 ? w.s.kv - 1 : min(rs.pos, w.s.kv - 1);
-      rs.slope_log2 = (valid && p.slopes) ? p.slopes[head] * kLog2e : 0.f;
-      // ---- Q row to shared memory, K-major with the 128-byte swizzle
+      rs.slope_log2 = (valid && p.slopes) ? p.slopes[qh] * kLog2e : 0.f;
+      // ---- Q row to shared memory, K-major with the 128-byte swizzle; blocks of the same rows write half of it each
       if (valid) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + token * p.q_stride + (int64_t)head * p.dq);
-        const int lo = p.dq < p.row ? (head & 1) * (p.dq / 8) : 0, hi = lo + p.dq / 8;  // map 2 in the upper half
-        const uint32_t dst = smem_addr(sQ) + r * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + token * p.q_stride + (int64_t)qh * p.dq);
+        const int lo = maps == 2 ? (qh & 1) * (p.dq / 8) : 0, hi = lo + p.dq / 8;  // map 2 in the upper half
+        const bool share = NB == 2 && !two;
+        const uint32_t dst = smem_addr(sQ) + (two ? blk * C::Q_BYTES : 0) + r * 128;
+        const int c0 = share ? blk * (D / 16) : 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          if (share && i >= D / 16) break;
+          const int c = c0 + i;
           uint4 v = make_uint4(0, 0, 0, 0);
           if (c >= lo && c < hi) v = __ldg(src + (c - lo));
           st_shared_v4(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4), v);
         }
       }
+      __syncwarp();
       fence_proxy_async_smem();
       tc_fence_before();  // the previous item's loads of O come before the product that overwrites it
       mbar_arrive(q_full);
-      // ---- key tiles
-      const int cnt = w.t1 - w.t0;
-      const bool warp_rows = quarters || warp * 32 < rows;
-      for (int i = 0; i < cnt; ++i, ++g) {
-        const int j0 = (w.t0 + i) * TK;
-        const uint32_t s_col = tmem + lane_base + (g & 1) * TK;
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + (g & 1), (g >> 1) & 1, status, kDevTimeoutSFull));
+      // ---- key tiles, from the last
+      const bool warp_rows = quarters || __any_sync(0xffffffffu, valid);
+      for (int s = 0; s < steps && ok; ++s) {
+        const int sb = NB == 2 ? blk : s & 1;  // S buffer
+        const uint32_t ph = NB == 2 ? sp0 + s : (sb ? sp1 : sp0) + (s >> 1);
+        const int i = NB == 1 || two ? s : 2 * s + blk;  // tile of the item
+        const int j0 = (w.t1 - 1 - i) * TK;
+        const uint32_t s_col = tmem + lanes + C::S_COL(sb);
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, ph & 1, status, kDevTimeoutSFull));
         if (!ok) break;
         tc_fence_after();
-        float alpha = 1.f;
-        if (quarters) {
-          constexpr int NC = TK / 4;
-          alpha = softmax_cols<T, NC>(p, rs, s_col, j0, warp * NC);
-          const uint32_t zero[NC / 2] = {};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q != warp) store_p<NC / 2>(s_col + q * (NC / 2), zero);
-        } else if (warp_rows) {  // the other warps' rows of P and O are read by nobody
-          alpha = softmax_cols<T, TK>(p, rs, s_col, j0, 0);
-        }
-        if (j0 + TK > w.s.kv) {
-          // slots past kvSeqLen may hold anything, NaN included, and 0 * NaN is not 0: clear their V rows
-          const int slot = g % NSV;
-          ok = __all_sync(0xffffffffu, mbar_wait(v_full + slot, (g / NSV) & 1, status, kDevTimeoutVFull));
+        if (s == 0 && blk == 0 && j0 + TK > w.s.kv) {
+          // slots past kvSeqLen may hold anything, NaN included, and 0 * NaN is not 0: clear their V rows.  Block 0
+          // has the first product of the item's first tile, so it does so for both.
+          const int slot = g0 % NSV;
+          ok = __all_sync(0xffffffffu, mbar_wait(v_full + slot, (g0 / NSV) & 1, status, kDevTimeoutVFull));
           if (!ok) break;
           if (r < TK && j0 + r >= w.s.kv) {
             const uint32_t dst = smem_addr(sV + slot * C::KV_BYTES) + r * 128;
@@ -749,101 +828,311 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 8; ++c) st_shared_v4(dst + cb * TK * 128 + c * 16, make_uint4(0, 0, 0, 0));
           }
+          __syncwarp();
           fence_proxy_async_smem();
         }
-        if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, status, kDevTimeoutODone));
-          if (!ok) break;
-          tc_fence_after();
+        // With two blocks O is at rest here: the product before this one had to finish before S was written.
+        auto rescale = [&](float alpha) {
+          if (s == 0 || !__any_sync(0xffffffffu, alpha != 1.f)) return true;
+          if constexpr (NB == 1) {
+            if (!__all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((sb ? sp0 : sp1) + ((s - 1) >> 1)) & 1, status,
+                                                   kDevTimeoutODone)))
+              return false;
+            tc_fence_after();
+          }
           scale_rows<D>(o_col, alpha);
+          return true;
+        };
+        auto half_done = [&](uint64_t* bar) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar);
+        };
+        uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+        if (quarters) {
+          constexpr int NC = TK / 4;
+          float x[NC];
+          load_cols<NC>(s_col + wq * NC, x);
+          const float alpha = grow(rs, scores<NC>(p, rs, x, j0 + wq * NC, raw_max));
+          ok = rescale(alpha);
+          if (!ok) break;
+          const float base = rs.m == -INFINITY ? 0.f : rs.m;
+          uint32_t pk[NC / 2];
+          exponentials<T, NC>(x, scale2, f2pack(-base, -base), acc, pk, carry && lane >= 16);
+          store_p<NC / 2>(s_col + wq * (NC / 2), pk);
+          const uint32_t zero[NC / 2] = {};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q != wq) store_p<NC / 2>(s_col + q * (NC / 2), zero);
+          rs.l = rs.l * alpha + sum4(acc);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_lo + sb);
+          mbar_arrive(p_full + sb);
+        } else if (warp_rows) {
+          // Half of the columns at a time, in 64 registers: the second half for its maximum, then the first for its
+          // maximum and its P, then the second again (P goes over the first half's scores only).
+          constexpr int NC = TK / 2;
+          float x[NC];
+          load_cols<NC>(s_col + NC, x);
+          float mx = scores<NC>(p, rs, x, j0 + NC, raw_max);
+          load_cols<NC>(s_col, x);
+          mx = fmaxf(mx, scores<NC>(p, rs, x, j0, raw_max));
+          const float alpha = grow(rs, mx);
+          ok = rescale(alpha);
+          if (!ok) break;
+          const float base = rs.m == -INFINITY ? 0.f : rs.m;
+          const uint64_t negm2 = f2pack(-base, -base);
+          uint32_t pk[NC / 2];
+          exponentials<T, NC>(x, scale2, negm2, acc, pk, false);
+          store_p<NC / 2>(s_col, pk);
+          load_cols<NC>(s_col + NC, x);
+          half_done(p_lo + sb);
+          scores<NC>(p, rs, x, j0 + NC, raw_max);
+          exponentials<T, NC>(x, scale2, negm2, acc, pk, false);
+          store_p<NC / 2>(s_col + NC / 2, pk);
+          half_done(p_full + sb);
+          rs.l = rs.l * alpha + sum4(acc);
+        } else {  // no row of the tile: what the lanes hold of P and O is read by nobody
+          mbar_arrive(p_lo + sb);
+          mbar_arrive(p_full + sb);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(p_full + (g & 1));
       }
-      if (!ok) break;
-      // o_done has one phase per item and is waited for once in each, so no wait can meet the phase before or
-      // after its own (pv_done may be two phases on, or one short, when a warp gets here)
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done, item & 1, status, kDevTimeoutODone));
-      ++item;
-      if (!ok) break;
+      g0 += cnt;
+      if constexpr (NB == 2) {
+        sp0 += steps;
+      } else {
+        sp0 += (steps + 1) >> 1;
+        sp1 += steps >> 1;
+      }
+      // o_done has one phase per item that the block took part in and is waited for once in each, so no wait can
+      // meet the phase before or after its own
+      if (steps > 0) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(o_done + blk, items & 1, status, kDevTimeoutODone));
+        ++items;
+      }
       tc_fence_after();
-      // ---- join the four lane quarters into the first: O' = sum_w 2^(m_w - M) O_w, l alike
+      const bool whole = w.t0 == 0 && w.t1 == w.n;
+      // partials: slot 1 when the item starts here, 0 when it began in an earlier CTA
+      const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * (NB * 128);
+      if (!whole && w.t0 == 0 && threadIdx.x == 0) {
+        // the last CTA c with c * total / ctas <= last tile
+        const int64_t last = line + w.n - 1;
+        PagedDesc d;
+        d.n_seg = (int)(((last + 1) * st.ctas - 1) / st.total) - (int)blockIdx.x + 1;
+        d.token0 = (int)token0;
+        d.tokens = tokens;
+        d.kv_head = w.h;
+        d.pos0 = w.rt * p.tb + off;
+        d.two = two;
+        p.desc[blockIdx.x] = d;
+        owner = true;
+      }
+      line += cnt;
       if (quarters) {
-        sML[warp * 32 + lane] = make_float2(rs.m, rs.l);
-        meet();
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) top = fmaxf(top, sML[q * 32 + lane].x);
-        const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum += sML[q * 32 + lane].y * fast_exp2(sML[q * 32 + lane].x - base);
-        const float f = fast_exp2(rs.m - base);
-        rs.m = top;
-        rs.l = sum;
-        // half of the columns at a time: 3 quarters x 32 rows x D / 2 floats fit the Q buffer
+        // ---- join the lane quarters of the blocks: O = sum_w 2^(m_w - M) O_w, l alike.  All warps leave some of
+        // their columns at a time in the Q buffers (4 NB x 32 rows x COLS floats fill them), then every thread
+        // sums 8 columns of a row over the quarters.
+        constexpr int NP = NB * 4, COLS = C::SCRATCH / (NP * 32 * 4), PASSES = D / COLS;
+        constexpr int CH = COLS / 8;  // 8-column chunks of a row in a pass
+        constexpr int NK = CH * 32 > NB * 128 ? CH * 32 / (NB * 128) : 1;
+        constexpr int F4 = COLS / 4;
         float4* scratch = reinterpret_cast<float4*>(sQ);
-        constexpr int F4 = D / 8;  // float4 chunks of half a row
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-          for (int c32 = 0; c32 < D / 64; ++c32) {
-            if (warp > 0) {
-              uint32_t regs[32];
-              tmem_ld32(o_col + half * (D / 2) + c32 * 32, regs);
-              tmem_ld_wait();
-              if (valid) {
+        const int rows = tokens * group;
+        const int me = blk * 4 + wq;
+        sM[me * 32 + lane] = rs.m;
+        meet();
+        float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const float4 v = make_float4(__uint_as_float(regs[4 * c]) * f, __uint_as_float(regs[4 * c + 1]) * f,
-                                               __uint_as_float(regs[4 * c + 2]) * f, __uint_as_float(regs[4 * c + 3]) * f);
-                  scratch[((warp - 1) * 32 + lane) * F4 + ((c32 * 8 + c) ^ (lane & 7))] = v;
+        for (int q = 0; q < NP; ++q) top = fmaxf(top, sM[q * 32 + lane]);
+        const float f = fast_exp2(rs.m - (top == -INFINITY ? 0.f : top));
+        float y[NK][PASSES][8], sum[NK];
+#pragma unroll
+        for (int pass = 0; pass < PASSES; ++pass) {
+#pragma unroll 1
+          for (int c32 = 0; c32 < COLS / 32; ++c32) {
+            uint32_t regs[32];
+            if (steps > 0) {
+              tmem_ld32(o_col + pass * COLS + c32 * 32, regs);
+              tmem_ld_wait();
+            }
+            if (valid) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (steps > 0)
+                  v = make_float4(__uint_as_float(regs[4 * c]) * f, __uint_as_float(regs[4 * c + 1]) * f,
+                                  __uint_as_float(regs[4 * c + 2]) * f, __uint_as_float(regs[4 * c + 3]) * f);
+                scratch[(me * 32 + lane) * F4 + ((c32 * 8 + c) ^ (lane & 7))] = v;
+              }
+            }
+            __syncwarp();
+          }
+          if (pass == PASSES - 1) sM[me * 32 + lane] = rs.l * f;  // every warp has read the maxima
+          meet();
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const int chunk = threadIdx.x + k * NB * 128, row = chunk / CH, c8 = chunk % CH;
+            float(&a)[8] = y[k][pass];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = 0.f;
+            if (pass == PASSES - 1) sum[k] = 0.f;
+            if (row < rows) {
+#pragma unroll
+              for (int q = 0; q < NP; ++q) {
+#pragma unroll
+                for (int up = 0; up < 2; ++up) {
+                  if (up == 1 && !carry) continue;
+                  const int at = row + up * 16;
+#pragma unroll
+                  for (int h4 = 0; h4 < 2; ++h4) {
+                    const float4 v = scratch[(q * 32 + at) * F4 + ((c8 * 2 + h4) ^ (at & 7))];
+                    a[4 * h4] += v.x;
+                    a[4 * h4 + 1] += v.y;
+                    a[4 * h4 + 2] += v.z;
+                    a[4 * h4 + 3] += v.w;
+                  }
                 }
+                if (pass == PASSES - 1) sum[k] += sM[q * 32 + row];
               }
             }
           }
           meet();
-          if (warp == 0) {
-#pragma unroll 1
-            for (int c32 = 0; c32 < D / 64; ++c32) {
-              uint32_t regs[32];
-              tmem_ld32(o_col + half * (D / 2) + c32 * 32, regs);
-              tmem_ld_wait();
-              if (valid) {
+        }
+        // ---- and its epilogue
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  float4 a = make_float4(__uint_as_float(regs[4 * c]) * f, __uint_as_float(regs[4 * c + 1]) * f,
-                                         __uint_as_float(regs[4 * c + 2]) * f, __uint_as_float(regs[4 * c + 3]) * f);
+        for (int k = 0; k < NK; ++k) {
+          const int chunk = threadIdx.x + k * NB * 128, row = chunk / CH, c8 = chunk % CH;
+          const float m = __shfl_sync(0xffffffffu, top, row & 31);
+          const bool mine = row < rows && ok;
+          if (!whole) {
+            if (mine) {
+              if (c8 == 0) p.ml[prow0 + row] = make_float2(m, sum[k]);
 #pragma unroll
-                  for (int q = 0; q < 3; ++q) {
-                    const float4 b = scratch[(q * 32 + lane) * F4 + ((c32 * 8 + c) ^ (lane & 7))];
-                    a.x += b.x;
-                    a.y += b.y;
-                    a.z += b.z;
-                    a.w += b.w;
-                  }
-                  regs[4 * c] = __float_as_uint(a.x);
-                  regs[4 * c + 1] = __float_as_uint(a.y);
-                  regs[4 * c + 2] = __float_as_uint(a.z);
-                  regs[4 * c + 3] = __float_as_uint(a.w);
-                }
+              for (int pass = 0; pass < PASSES; ++pass)
+                if (pass * COLS + c8 * 8 < p.row)
+                  st_global_v8(p.part + (prow0 + row) * D + pass * COLS + c8 * 8, reinterpret_cast<uint32_t*>(y[k][pass]));
+            }
+            continue;
+          }
+          const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;  // a row without keys gets 0
+          const int64_t t = token0 + row / group;
+          const int h = w.h * group + row % group;
+          float post = inv;
+          if (maps == 2) {
+            // rows 2i and 2i + 1 are the two maps of a head, CH lanes apart
+            const float wgt = !mine ? 0.f : (row & 1) ? -p.lambda[h >> 1] * inv : inv;
+            float ss = 0.f;
+#pragma unroll
+            for (int pass = 0; pass < PASSES; ++pass)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float v = y[k][pass][i] * wgt;
+                v += __shfl_xor_sync(0xffffffffu, v, CH);
+                if (pass * COLS + c8 * 8 >= p.row) v = 0.f;
+                y[k][pass][i] = v;
+                ss = fmaf(v, v, ss);
               }
-              __syncwarp();
-              tmem_st32(o_col + half * (D / 2) + c32 * 32, regs);
+            post = p.out_scale;
+            if (p.norm_weight) {
+#pragma unroll
+              for (int o = 1; o < CH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+              post = p.out_scale * rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
+            }
+          }
+#pragma unroll
+          for (int pass = 0; pass < PASSES; ++pass) {
+            const int col = pass * COLS + c8 * 8;
+            // of the two lanes that hold a differential row, the even one stores the even passes
+            if (!mine || col >= p.row || (maps == 2 && (row & 1) != (pass & 1))) continue;
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float a = y[k][pass][2 * i] * post, b = y[k][pass][2 * i + 1] * post;
+              if (maps == 2 && p.norm_weight) {
+                a *= __ldg(p.norm_weight + col + 2 * i);
+                b *= __ldg(p.norm_weight + col + 2 * i + 1);
+              }
+              o[i] = pack2(a, b, (T*)nullptr);
+            }
+            st_global_v4(static_cast<T*>(p.out) + (t * (p.heads / maps) + h / maps) * p.row + col, o);
+          }
+          if (mine && p.lse && c8 == 0) {
+            float lse = sum[k] > 0.f ? m * kLn2 + logf(sum[k]) : -INFINITY;
+            if (p.mask_type == 5) lse += p.slopes[h] * static_cast<float>(w.rt * p.tb + row / group + off);
+            p.lse[t * p.heads + h] = lse;
+          }
+        }
+        continue;
+      }
+      bool has_rows = warp_rows;
+      float* exchange = reinterpret_cast<float*>(sQ);  // a row of XCOLS floats for each thread, chunks swizzled by the row
+      constexpr int XCOLS = C::SCRATCH / (128 * 4) < D ? C::SCRATCH / (128 * 4) : D;
+      auto slot4 = [&](int c4) { return reinterpret_cast<float4*>(exchange + (size_t)r * XCOLS) + (c4 ^ (r & 7)); };
+      if (NB == 2 && !two) {
+        // ---- the blocks hold the same rows: block 1 hands its row to block 0, through the Q buffers, once block 0's
+        // last score product has read those too
+        float f0 = 1.f, f1 = 0.f;
+#pragma unroll 1
+        for (int x0 = 0; x0 < D; x0 += XCOLS) {
+          meet();
+          if (blk == 1) {
+            if (x0 == 0) {
+              sM[r] = rs.m;
+              sM[128 + r] = rs.l;
+            }
+            if (warp_rows) {
+#pragma unroll 1
+              for (int c32 = 0; c32 < XCOLS / 32; ++c32) {
+                uint32_t regs[32];
+                if (steps > 0) {
+                  tmem_ld32(o_col + x0 + c32 * 32, regs);
+                  tmem_ld_wait();
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *slot4(c32 * 8 + c) = steps == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                   : make_float4(__uint_as_float(regs[4 * c]), __uint_as_float(regs[4 * c + 1]),
+                                                                 __uint_as_float(regs[4 * c + 2]), __uint_as_float(regs[4 * c + 3]));
+              }
+            }
+          }
+          meet();
+          if (blk == 0 && warp_rows) {
+            if (x0 == 0) {
+              const float m1 = sM[r], l1 = sM[128 + r], top = fmaxf(rs.m, m1), base = top == -INFINITY ? 0.f : top;
+              f0 = fast_exp2(rs.m - base);
+              f1 = fast_exp2(m1 - base);
+              rs.l = rs.l * f0 + l1 * f1;
+              rs.m = top;
+            }
+#pragma unroll 1
+            for (int c32 = 0; c32 < XCOLS / 32; ++c32) {
+              uint32_t regs[32];
+              tmem_ld32(o_col + x0 + c32 * 32, regs);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 v = *slot4(c32 * 8 + c);
+                regs[4 * c] = __float_as_uint(fmaf(v.x, f1, __uint_as_float(regs[4 * c]) * f0));
+                regs[4 * c + 1] = __float_as_uint(fmaf(v.y, f1, __uint_as_float(regs[4 * c + 1]) * f0));
+                regs[4 * c + 2] = __float_as_uint(fmaf(v.z, f1, __uint_as_float(regs[4 * c + 2]) * f0));
+                regs[4 * c + 3] = __float_as_uint(fmaf(v.w, f1, __uint_as_float(regs[4 * c + 3]) * f0));
+              }
+              tmem_st32(o_col + x0 + c32 * 32, regs);
             }
             tmem_st_wait();
           }
-          meet();
         }
+        meet();  // the exchange has been read: the next item's Q may go there
+        has_rows = has_rows && blk == 0;
       }
-      if (!ok) break;
-      // ---- epilogue
-      const bool whole = w.t0 == 0 && w.t1 == w.n;
-      const bool has_rows = warp_rows && (!quarters || warp == 0);
+      // ---- epilogue, a thread a row
+      has_rows = has_rows && ok;
+      const float inv_l = rs.l > 0.f ? 1.f / rs.l : 0.f;  // a row without keys gets 0
       if (!whole) {
-        // a cut item: unnormalised O, max and sum; slot 1 when the item starts here, 0 when it began earlier
-        const int64_t prow = ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * 128 + rr;
         if (has_rows) {
+          const int64_t prow = prow0 + (two ? blk * 128 : 0) + r;
           if (valid) p.ml[prow] = make_float2(rs.m, rs.l);
           float* dst = p.part + prow * D;
 #pragma unroll 1
@@ -856,24 +1145,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) st_global_v8(dst + c32 * 32 + i * 8, regs + i * 8);
             }
+            __syncwarp();
           }
         }
-        if (w.t0 == 0 && threadIdx.x == 0) {
-          // the last CTA c with c * total / ctas <= last tile
-          const int64_t last = line + w.n - 1;
-          PagedDesc d;
-          d.n_seg = (int)(((last + 1) * st.ctas - 1) / st.total) - (int)blockIdx.x + 1;
-          d.token0 = (int)(w.cu + w.rt * p.tb);
-          d.rows = rows;
-          d.kv_head = w.h;
-          d.pos0 = w.rt * p.tb + off;
-          p.desc[blockIdx.x] = d;
-          owner = true;
-        }
-      } else if (has_rows) {
-        const float inv_l = rs.l > 0.f ? 1.f / rs.l : 0.f;  // a row without keys gets 0
-        if (p.dq == p.row) {
-          T* orow = static_cast<T*>(p.out) + (token * p.heads + head) * p.row;
+      } else if (maps == 1) {
+        if (has_rows) {
+          T* orow = static_cast<T*>(p.out) + (token * p.heads + qh) * p.row;
           const bool wide = p.row % 16 == 0;
 #pragma unroll 1
           for (int c32 = 0; c32 < D / 32; ++c32) {
@@ -895,27 +1172,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (c32 * 32 + i * 8 < p.row) st_global_v4(orow + c32 * 32 + i * 8, o + i * 4);
               }
             }
+            __syncwarp();
           }
           if (valid && p.lse) {
             float lse = rs.l > 0.f ? rs.m * kLn2 + logf(rs.l) : -INFINITY;
-            if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(rs.pos);  // left-aligned = right-aligned + slope * pos
-            p.lse[token * p.heads + head] = lse;
+            if (p.mask_type == 5) lse += p.slopes[qh] * static_cast<float>(rs.pos);  // left-aligned = right-aligned + slope * pos
+            p.lse[token * p.heads + qh] = lse;
           }
-        } else {
-          // even lanes hold map 1, odd lanes map 2 of the same head: even lanes finish the first 16 columns of
-          // each 32, odd lanes the others
-          const bool odd = lane & 1;
-          const int oh = head >> 1;
-          const float f = odd ? (valid ? -p.lambda[oh] * inv_l : 0.f) : inv_l;
-          float y[16];
+        }
+      } else {
+        // the difference of the maps, in 16-column groups: of neighbouring lanes (even: map 1) where they are
+        // neighbouring rows, the even lane finishing the first 16 columns of each 32 and the odd lane the others;
+        // of the two blocks' rows, through the exchange, where a block is a map
+        const int oh = qh >> 1;
+        const float f = !valid ? 0.f : (qh & 1) ? -p.lambda[oh] * inv_l : inv_l;
+        const bool odd = !two && (lane & 1);
+        if (two) {
+          if (blk == 1 && has_rows) {
+#pragma unroll 1
+            for (int c32 = 0; c32 < D / 32; ++c32) {
+              uint32_t regs[32];
+              tmem_ld32(o_col + c32 * 32, regs);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *slot4(c32 * 8 + c) = make_float4(__uint_as_float(regs[4 * c]) * f, __uint_as_float(regs[4 * c + 1]) * f,
+                                                  __uint_as_float(regs[4 * c + 2]) * f, __uint_as_float(regs[4 * c + 3]) * f);
+            }
+          }
+          meet();
+        }
+        if (has_rows && !(two && blk == 1)) {
+          constexpr int kMost = 32;
+          float y[kMost];
+          // y: the columns of this thread from c32 * 32 (two blocks: all 32; else 16 of them)
           auto diff = [&](int c32) {
             uint32_t regs[32];
             tmem_ld32(o_col + c32 * 32, regs);
             tmem_ld_wait();
+            if (two) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = __uint_as_float(regs[i]) * f, b = __uint_as_float(regs[16 + i]) * f;
-              y[i] = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              for (int c = 0; c < 8; ++c) {
+                const float4 v = *slot4(c32 * 8 + c);
+                y[4 * c] = fmaf(__uint_as_float(regs[4 * c]), f, v.x);
+                y[4 * c + 1] = fmaf(__uint_as_float(regs[4 * c + 1]), f, v.y);
+                y[4 * c + 2] = fmaf(__uint_as_float(regs[4 * c + 2]), f, v.z);
+                y[4 * c + 3] = fmaf(__uint_as_float(regs[4 * c + 3]), f, v.w);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float a = __uint_as_float(regs[i]) * f, b = __uint_as_float(regs[16 + i]) * f;
+                y[i] = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              }
             }
           };
           float post = p.out_scale;
@@ -923,23 +1232,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ss = 0.f;
 #pragma unroll 1
             for (int c32 = 0; c32 < D / 32; ++c32) {
+              if (c32 * 32 >= p.row) break;
               diff(c32);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+              for (int i = 0; i < kMost; ++i) {
+                const int col = c32 * 32 + (odd ? 16 : 0) + i;
+                if ((two || i < 16) && col < p.row) ss = fmaf(y[i], y[i], ss);
+              }
             }
-            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            if (!two) ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
           }
           T* orow = static_cast<T*>(p.out) + (token * (p.heads / 2) + oh) * p.row;
 #pragma unroll 1
           for (int c32 = 0; c32 < D / 32; ++c32) {
-            const int col = c32 * 32 + (odd ? 16 : 0);
+            if (c32 * 32 >= p.row) break;
             diff(c32);
-            if (valid && col < p.row) {
+#pragma unroll
+            for (int i16 = 0; i16 < 2; ++i16) {
+              const int col = c32 * 32 + (odd ? 16 : i16 * 16);
+              if (!valid || col >= p.row || (!two && i16 == 1)) continue;
               uint32_t o[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                float a = y[2 * i] * post, b = y[2 * i + 1] * post;
+                float a = y[i16 * 16 + 2 * i] * post, b = y[i16 * 16 + 2 * i + 1] * post;
                 if (p.norm_weight) {
                   a *= __ldg(p.norm_weight + col + 2 * i);
                   b *= __ldg(p.norm_weight + col + 2 * i + 1);
@@ -948,17 +1264,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               st_global_v8(orow + col, o);
             }
+            __syncwarp();
           }
         }
+        if (two) meet();  // the exchange has been read
       }
-      line += cnt;
     } while (w.next(p));
     if (threadIdx.x == 0 && !owner) p.desc[blockIdx.x].n_seg = 0;
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 6) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -991,20 +1309,20 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedDesc d = p.desc[blockIdx.x];
   if (d.n_seg == 0) return;
+  constexpr int NB = D == 256 ? 1 : 2;
   constexpr int N = D / 32;                   // columns per lane
   constexpr int NW = (kGrid + 31) / 32;       // segment weights per lane
   const int lane = threadIdx.x & 31;
-  const int maps = p.dq == p.row ? 1 : 2;
+  const int maps = p.maps(), gh = p.group / maps;
   const int col = lane * N;
-  for (int u = blockIdx.y * 8 + (threadIdx.x >> 5); u * maps < d.rows; u += kCombineY * 8) {
+  for (int u = blockIdx.y * 8 + (threadIdx.x >> 5); u < d.tokens * gh; u += kCombineY * 8) {
     float y[N];
     float lse = 0.f;
-    const int r0 = u * maps;
-    const int token = d.token0 + r0 / p.group, head = d.kv_head * p.group + r0 % p.group;
+    const int tok = u / gh, token = d.token0 + tok, head = (d.kv_head * gh + u % gh) * maps;
     for (int map = 0; map < maps; ++map) {
-      const int r = r0 + map;
+      const int r = partial_row(p, d.two, tok, u % gh, map);
       // segment s lies in CTA blockIdx.x + s: in its slot 1 where the item starts, in slot 0 after that
-      auto prow = [&](int s) { return ((int64_t)(blockIdx.x + s) * 2 + (s == 0 ? 1 : 0)) * 128 + r; };
+      auto prow = [&](int s) { return ((int64_t)(blockIdx.x + s) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r; };
       float wt[NW], top = -INFINITY, sum = 0.f;
       float2 ml[NW];
 #pragma unroll
@@ -1064,7 +1382,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
 #pragma unroll
       for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);
     } else if (p.lse && lane == 0) {
-      if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + r0 / p.group);
+      if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + tok);
       p.lse[(int64_t)token * p.heads + head] = lse;
     }
     if (col < p.row) {
@@ -1079,15 +1397,23 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   }
 }
 
-template <typename T, int D>
-cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, cudaStream_t stream) {
-  using C = Cfg<T, D>;
+template <typename T, int D, int NQ>
+cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, cudaStream_t stream) {
+  using C = Cfg<T, D, NQ>;
   // at least 120 KB so a second CTA never shares the SM (each CTA allocates all 512 TMEM columns)
   constexpr int kSmem = C::SMEM > 120 * 1024 ? C::SMEM : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<T, D><<<kGrid, kThreads, kSmem, stream>>>(tmK, tmV, p);
-  e = cudaGetLastError();
+  paged_attn_kernel<T, D, NQ><<<kGrid, C::THREADS, kSmem, stream>>>(tmK, tmV, p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool two, cudaStream_t stream) {
+  cudaError_t e;
+  if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
+  else if constexpr (D == 64) e = launch_attn<T, D, 2>(tmK, tmV, p, stream);
+  else e = two ? launch_attn<T, D, 2>(tmK, tmV, p, stream) : launch_attn<T, D, 1>(tmK, tmV, p, stream);
   if (e != cudaSuccess) return e;
   // a programmatic dependent launch: the combine grid is scheduled during the attention kernel's tail, and
   // griddepcontrol.wait holds it until that kernel has completed
@@ -1113,11 +1439,11 @@ int paged_kernel_d(int64_t row) {
 }
 
 void paged_layout(PagedPlan* plan) {
-  const int D = paged_kernel_d(plan->row);
+  const int D = paged_kernel_d(plan->row), rows = D == 256 ? 128 : 256;
   plan->off_desc = kPagedStatusBytes;
   plan->off_ml = align256(plan->off_desc + sizeof(PagedDesc) * kGrid);
-  plan->off_part = align256(plan->off_ml + sizeof(float2) * kGrid * 2 * 128);
-  plan->ws_size = plan->off_part + (uint64_t)sizeof(float) * kGrid * 2 * 128 * D;
+  plan->off_part = align256(plan->off_ml + sizeof(float2) * kGrid * 2 * rows);
+  plan->ws_size = plan->off_part + (uint64_t)sizeof(float) * kGrid * 2 * rows * D;
 }
 
 int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, size_t errlen) {
@@ -1126,8 +1452,11 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
   const int box = kv_box_rows(plan->block_size, D == 256 ? 64 : 128);
   if (!plan->maps_ready) {
     const int64_t rows = (int64_t)plan->num_blocks * plan->block_size;
-    if (!encode_rows_heads_d(&plan->tmK, plan->k, plan->dtype, rows, plan->kv_heads, plan->row, box, false) ||
-        !encode_rows_heads_d(&plan->tmV, plan->v, plan->dtype, rows, plan->kv_heads, plan->row, box, true)) {
+    // L2 fetches whole lines of a kv head's row and no more: a line that reaches into the next head's row is gone
+    // from L2 when its turn comes
+    const int bytes = plan->row * 2, promote = bytes % 256 == 0 ? 256 : bytes % 128 == 0 ? 128 : 0;
+    if (!encode_rows_heads_d(&plan->tmK, plan->k, plan->dtype, rows, plan->kv_heads, plan->row, box, false, promote) ||
+        !encode_rows_heads_d(&plan->tmV, plan->v, plan->dtype, rows, plan->kv_heads, plan->row, box, true, promote)) {
       snprintf(err, errlen, "cuTensorMapEncodeTiled failed");
       return ALA_CUDA_ERROR;
     }
@@ -1161,20 +1490,24 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     p.heads = plan->heads;
     p.kv_heads = plan->kv_heads;
     p.group = plan->heads / plan->kv_heads;
-    p.tb = 128 / p.group;
     p.dq = plan->d;
     p.row = plan->row;
+    p.tb1 = 128 / p.group;
+    // Two blocks of rows where sequences have more than one block's on average (the lengths are on the device; any
+    // lengths run on either); at D = 64 there is room for both Q blocks and deep rings anyway.
+    const bool two = D == 64 || (D == 128 && plan->n_tokens * p.group > (int64_t)128 * p.batch);
+    p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
     p.box_rows = box;
     p.scale_log2 = plan->qk_scale * kLog2e;
     p.norm_eps = plan->norm_eps;
     p.out_scale = plan->out_scale;
     const bool f16 = plan->dtype == ALA_F16;
     if (D == 64)
-      e = f16 ? launch<__half, 64>(plan->tmK, plan->tmV, p, stream) : launch<__nv_bfloat16, 64>(plan->tmK, plan->tmV, p, stream);
+      e = f16 ? launch<__half, 64>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 64>(plan->tmK, plan->tmV, p, two, stream);
     else if (D == 128)
-      e = f16 ? launch<__half, 128>(plan->tmK, plan->tmV, p, stream) : launch<__nv_bfloat16, 128>(plan->tmK, plan->tmV, p, stream);
+      e = f16 ? launch<__half, 128>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 128>(plan->tmK, plan->tmV, p, two, stream);
     else
-      e = f16 ? launch<__half, 256>(plan->tmK, plan->tmV, p, stream) : launch<__nv_bfloat16, 256>(plan->tmK, plan->tmV, p, stream);
+      e = f16 ? launch<__half, 256>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 256>(plan->tmK, plan->tmV, p, two, stream);
   }
   if (e != cudaSuccess) {
     snprintf(err, errlen, "kernel launch failed: %s", cudaGetErrorString(e));

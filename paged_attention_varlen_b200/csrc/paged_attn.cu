@@ -35,76 +35,18 @@
 //   then a warp each      TMA producer of the K ring, of the V ring (lane i gathers box i of a tile through
 //                         the block table), and the tcgen05 issuer: S_b = Q K^T, O_b += P_b V with P_b read
 //                         from TMEM over S_b, P V in two halves of the keys
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
-#include "internal.h"
-#include "paged.h"
-#include "ptx.cuh"
+#include "paged_common.cuh"
 
 namespace ala {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
-constexpr int kGrid = 148;                 // one CTA per SM of a B200
 constexpr int kCombineY = 4;               // blocks per segment list in the combine grid
-
-// What a split item's first CTA leaves for the combine kernel.
-struct PagedDesc {
-  int32_t n_seg;    // CTAs that hold a segment of the item (0: this CTA starts no split item)
-  int32_t token0;   // first token of the row tile
-  int32_t tokens;   // its tokens
-  int32_t kv_head;
-  int32_t pos0;     // absolute position of token0
-  int32_t two;      // rows in two blocks
-};
-
-struct PagedParams {
-  const int32_t *seq_len, *kv_seq_len, *block_tables;
-  const float *slopes, *lambda, *norm_weight;
-  const void* q;
-  void* out;
-  float* lse;
-  int* status;
-  PagedDesc* desc;  // [kGrid]
-  float2* ml;       // [kGrid][2][128 NB]: running max (log2 units) and sum of each partial row
-  float* part;      // [kGrid][2][128 NB][D]
-  int64_t q_stride;
-  int32_t n_tokens, batch, max_blocks, block_size, num_blocks, mask_type;
-  int32_t heads, group, kv_heads;  // query heads, per kv head (both maps counted)
-  int32_t tb1, tb;                 // tokens of one block of rows (128 / group), tokens per row tile
-  int32_t dq, row;                 // query head size, elements of a K / V row
-  int32_t box_rows;
-  float scale_log2, norm_eps, out_scale;
-
-  __host__ __device__ int maps() const { return dq == row ? 1 : 2; }
-};
-
-// Row of an item's partials that holds (token of the tile, head of the group without its map, map).
-__device__ __forceinline__ int partial_row(const PagedParams& p, bool two, int token, int hh, int map) {
-  const int maps = p.maps();
-  if (!two) return token * p.group + hh * maps + map;
-  if (maps == 2) return map * 128 + token * (p.group / 2) + hh;
-  return token < p.tb1 ? token * p.group + hh : 128 + (token - p.tb1) * p.group + hh;
-}
-
-template <typename T>
-struct ElemFmt;
-template <>
-struct ElemFmt<__half> {
-  static constexpr uint32_t fmt = 0;
-};
-template <>
-struct ElemFmt<__nv_bfloat16> {
-  static constexpr uint32_t fmt = 1;
-};
 
 // The rings fill what shared memory leaves: a tile arrives a few thousand cycles after its load is issued, so
 // depth is what keeps HBM busy.
@@ -122,7 +64,7 @@ struct Cfg {
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int SCRATCH = NQ * Q_BYTES;    // the Q buffers between items: what the joins pass through
   static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 4 * 2 + 2 + 1;
-  static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;
+  static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;  // 256 floats: sM
   static constexpr uint32_t S_COL(int b) { return b * TK; }
   static constexpr uint32_t O_COL(int b) { return 2 * TK + (NB == 2 ? b * D : 0); }
   static constexpr uint32_t TMEM_COLS = 512;
@@ -131,286 +73,23 @@ struct Cfg {
   static_assert(2 * TK + NB * D <= TMEM_COLS, "tensor memory budget");
 };
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* a) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]),
-               "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
-               : "memory");
-}
-__device__ __forceinline__ void st_global_v4(void* p, const uint32_t* a) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]) : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16*) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half*) {
-  __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float2 unpack2(uint32_t v, __nv_bfloat16*) {
-  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t v, __half*) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
-
-// ---------------------------------------------------------------------------------------------- the work line
-
-// One sequence as the kernel takes it: lengths outside what the tensors hold are cut to it.
-struct Seq {
-  int seq, kv, tiles;  // new tokens, keys, row tiles
-};
-
-__device__ __forceinline__ int raw_len(const PagedParams& p, int b) { return min(max(__ldg(p.seq_len + b), 0), p.n_tokens); }
-
-__device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, int64_t cu, int raw) {
-  Seq s;
-  s.seq = cu >= p.n_tokens ? 0 : (int)min((int64_t)raw, p.n_tokens - cu);
-  const int64_t room = (int64_t)p.max_blocks * p.block_size;
-  s.kv = (int)min((int64_t)max(__ldg(p.kv_seq_len + b), 0), room);
-  s.tiles = (s.seq + p.tb - 1) / p.tb;
-  return s;
-}
-
-// Key tiles of row tile `rt`: up to the last key its last token may see, and at least one, so that rows
-// without keys are written too.
-template <int TK>
-__device__ __forceinline__ int key_tiles(const PagedParams& p, const Seq& s, int rt) {
-  int64_t keys = s.kv;
-  if (p.mask_type != 0) {
-    const int64_t end = min((int64_t)(rt + 1) * p.tb, (int64_t)s.seq) + s.kv - s.seq;
-    keys = max((int64_t)0, min(end, (int64_t)s.kv));
-  }
-  return max(1, (int)((keys + TK - 1) / TK));
-}
-
-// sum over i < n of floor((a i + b) / m), by Euclid's steps on (a, m)
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint64_t b) {
-  uint64_t s = 0;
-  for (;;) {
-    if (a >= m) {
-      s += (uint64_t)n * (n - 1u) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      s += n * (b / m);
-      b %= m;
-    }
-    const uint64_t y = (uint64_t)a * n + b;
-    if (n == 0 || y < m) return (int64_t)s;
-    n = (uint32_t)(y / m);
-    b = y % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
-  }
-}
-
-// Key tiles of the first r row tiles of one kv head.
-template <int TK>
-__device__ int64_t tiles_before(const PagedParams& p, const Seq& s, int r) {
-  if (r == 0) return 0;
-  if (p.mask_type == 0) return (int64_t)r * key_tiles<TK>(p, s, 0);
-  int64_t last = 0;
-  if (r == s.tiles) {  // the last row tile may be short
-    last = key_tiles<TK>(p, s, r - 1);
-    --r;
-  }
-  // full row tile i (from 1) sees off + i tb keys: one tile while that is at most TK, then ceil(. / TK)
-  const int64_t off = (int64_t)s.kv - s.seq;
-  int64_t ones = off >= TK ? 0 : (TK - off) / p.tb;
-  ones = min(ones, (int64_t)r);
-  const int64_t m = r - ones;
-  return last + ones + (m > 0 ? floor_sum((uint32_t)m, TK, p.tb, (uint64_t)(off + (ones + 1) * p.tb + TK - 1)) : 0);
-}
-
-// A CTA's position on the work line: item (b, h, rt) and its tiles [t0, t1) of n.
-template <int TK>
-struct Walker {
-  int b, h, rt, t0, t1, n;
-  int raw;
-  int64_t cu, left;
-  Seq s;
-
-  __device__ __forceinline__ void enter(const PagedParams& p) {
-    n = key_tiles<TK>(p, s, rt);
-    t1 = (int)min((int64_t)n, t0 + left);
-  }
-  __device__ __forceinline__ bool next(const PagedParams& p) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
-    t0 = 0;
-    if (++rt == s.tiles) {
-      rt = 0;
-      if (++h == p.kv_heads) {
-        h = 0;
-        do {
-          cu += raw;
-          if (++b >= p.batch) return false;
-          raw = raw_len(p, b);
-          s = load_seq(p, b, cu, raw);
-        } while (s.seq == 0);
-      }
-    }
-    enter(p);
-    return true;
-  }
-  __device__ __forceinline__ int tokens(const PagedParams& p) const { return min(p.tb, s.seq - rt * p.tb); }
-};
-
-struct Start {
-  int b, h, rt, t0, raw;
-  int64_t cu, left, line, total;  // line: this CTA's first tile on the line of `total` tiles
-  int ctas;                       // CTAs that take part
-};
-
-// Every thread of the CTA scans the batch (kThreads sequences at a time); the results are in *st after the
-// caller's __syncthreads.  `red` holds 2 * kThreads / 32 words.
-template <int TK, int kThreads>
-__device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = kThreads / 32;
-  int64_t cu0 = 0, w0 = 0;  // tokens and tiles before this chunk
-  int64_t start = 0, end = 0;
-  int raw = 0;
-  int64_t cu = 0, w_before = 0, w = 0;
-  Seq s{0, 0, 0};
-  // a chunk: each thread's sequence, the tokens before it and the tiles before it
-  auto scan = [&](int b0) {
-    const int b = b0 + threadIdx.x;
-    raw = b < p.batch ? raw_len(p, b) : 0;
-    int64_t x = raw;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) red[warp] = x;
-    __syncthreads();
-    int64_t before = cu0, sum = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += red[i];
-      sum += red[i];
-    }
-    cu = before + x - raw;
-    cu0 += sum;
-    w = 0;
-    if (b < p.batch) {
-      s = load_seq(p, b, cu, raw);
-      if (s.seq > 0) w = tiles_before<TK>(p, s, s.tiles) * p.kv_heads;
-      if (blockIdx.x == 0 && (raw != __ldg(p.seq_len + b) || s.seq != raw || s.kv != __ldg(p.kv_seq_len + b)))
-        atomicCAS(p.status + 1, 0, kDevBadLength);
-    }
-    x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) red[kWarps + warp] = x;
-    __syncthreads();
-    before = w0;
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += red[kWarps + i];
-      sum += red[kWarps + i];
-    }
-    w_before = before + x - w;
-    w0 += sum;
-    __syncthreads();
-  };
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) scan(b0);
-  const int64_t total = w0;
-  const int ctas = (int)min((int64_t)gridDim.x, total);
-  if (threadIdx.x == 0) {
-    st->total = total;
-    st->ctas = ctas;
-    st->b = -1;
-  }
-  if ((int)blockIdx.x >= ctas) return;
-  start = blockIdx.x * total / ctas;
-  end = (blockIdx.x + 1) * total / ctas;
-  __syncthreads();
-  auto place = [&](int b0) {
-    if (w > 0 && w_before <= start && start < w_before + w) {
-      st->b = b0 + threadIdx.x;
-      st->raw = raw;
-      st->cu = cu;
-      st->line = start;
-      st->left = end - start;
-      const int64_t per_head = w / p.kv_heads;
-      st->h = (int)((start - w_before) / per_head);
-      red[0] = start - w_before - st->h * per_head;  // tile within the head
-    }
-  };
-  if (p.batch <= kThreads) {
-    place(0);
-  } else {
-    cu0 = w0 = 0;
-    for (int b0 = 0; b0 < p.batch && w0 <= start; b0 += kThreads) {
-      scan(b0);
-      place(b0);
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const int b = st->b;
-    const Seq q = load_seq(p, b, st->cu, st->raw);
-    const int64_t tile = red[0];
-    int lo = 0, hi = q.tiles;  // the row tile lies in [lo, hi): 32 candidates a round
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int c = lo + (lane + 1) * step;
-      const bool below = c < hi && tiles_before<TK>(p, q, c) <= tile;
-      const int k = __popc(__ballot_sync(0xffffffffu, below));
-      lo += k * step;
-      hi = min(hi, lo + step);
-    }
-    if (lane == 0) {
-      st->rt = lo;
-      st->t0 = (int)(tile - tiles_before<TK>(p, q, lo));
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------------------------- softmax
 
 template <int NC>
 __device__ __forceinline__ void load_cols(uint32_t col, float (&x)[NC]) {
-  if constexpr (NC >= 32) {
-    uint32_t r[NC / 32][32];
+  uint32_t r[NC / 32][32];
 #pragma unroll
-    for (int i = 0; i < NC / 32; ++i) tmem_ld32(col + i * 32, r[i]);
-    tmem_ld_wait();  // one wait for all loads
+  for (int i = 0; i < NC / 32; ++i) tmem_ld32(col + i * 32, r[i]);
+  tmem_ld_wait();  // one wait for all loads
 #pragma unroll
-    for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
-  } else {
-    uint32_t r[16];
-    tmem_ld16(col, r);
-    tmem_ld_wait();
-#pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(r[c]);
-  }
+  for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
 }
 
-// NC / 2 packed columns of P
+// N packed columns of P
 template <int N>
 __device__ __forceinline__ void store_p(uint32_t col, const uint32_t (&pk)[N]) {
-  if constexpr (N >= 32) {
-#pragma unroll
-    for (int i = 0; i < N / 32; ++i) {
-      uint32_t t[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) t[c] = pk[i * 32 + c];
-      tmem_st32(col + i * 32, t);
-    }
-  } else if constexpr (N == 16) {
-    tmem_st16(col, pk);
-  } else {
-    tmem_st8(col, pk);
-  }
+  if constexpr (N == 32) tmem_st32(col, pk);
+  else tmem_st16(col, pk);
 }
 
 // What a row keeps over an item.
@@ -475,10 +154,10 @@ __device__ __forceinline__ float grow(RowState& rs, float mx) {
 
 // P = 2^(x - m) of N columns, packed; adds to the four partial sums.  P is rounded to the operand
 // type of the tensor core; the sum takes the unrounded values, so a row's rounding errors (at most half a step
-// of each weight) average out instead of biasing the normalisation.  `rest`: the part that rounding drops.
+// of each weight) average out instead of biasing the normalisation.
 template <typename T, int N>
 __device__ __forceinline__ void exponentials(const float (&x)[N], uint64_t scale2, uint64_t negm2, uint64_t (&acc)[4],
-                                             uint32_t (&pk)[N / 2], bool rest) {
+                                             uint32_t (&pk)[N / 2]) {
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
     float e0, e1;
@@ -487,12 +166,6 @@ __device__ __forceinline__ void exponentials(const float (&x)[N], uint64_t scale
     e1 = fast_exp2(e1);
     acc[(c >> 1) & 3] = add_x2(acc[(c >> 1) & 3], f2pack(e0, e1));
     pk[c / 2] = pack2(e0, e1, (T*)nullptr);
-    if constexpr (N <= 32) {
-      if (rest) {
-        const float2 r = unpack2(pk[c / 2], (T*)nullptr);
-        pk[c / 2] = pack2(e0 - r.x, e1 - r.y, (T*)nullptr);
-      }
-    }
   }
 }
 
@@ -552,7 +225,6 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   int* status = p.status;
   constexpr int kWarpK = NB * 4, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 
-  find_start<TK, C::THREADS>(p, &st, red);
   if (threadIdx.x == 0) {
     mbar_init(q_full, NB * 128);
     for (int s = 0; s < NSK; ++s) {
@@ -573,6 +245,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     mbar_init(fin, 1);
     fence_mbar_init();
   }
+  find_start<TK, C::THREADS>(p, &st, red);
   __syncthreads();
   if (st.b < 0) {  // fewer tiles than CTAs
     if (threadIdx.x == 0) p.desc[blockIdx.x].n_seg = 0;
@@ -595,7 +268,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   w.raw = st.raw;
   w.cu = st.cu;
   w.left = st.left;
-  w.s = load_seq(p, w.b, w.cu, w.raw);
+  w.s = st.s;
+  w.fetch(p);
   w.enter(p);
 
   // An item of cnt tiles is U steps: step u fills S buffer u & 1 and multiplies its P.  With two blocks of rows,
@@ -662,8 +336,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       mbar_wait(full_bar + (i % depth), (i / depth) & 1, status, is_k ? kDevTimeoutKFull : kDevTimeoutVFull);
     __syncwarp();
   } else if (warp == kWarpMma) {
-    // -------------------------------------------------------------- MMA issuer
-    const bool leader = elect_one();
+    // -------------------------------------------------------------- MMA issuer: one thread
+    if (lane == 0) {
     const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_addr(sV), TK * 128, 1024);  // MN-major
@@ -671,75 +345,88 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     constexpr uint32_t kIdescQk = instr_desc(ElemFmt<T>::fmt, false, false, 128, TK);
     // P V makes the row's columns only, rounded up to the instruction's step of 16
     const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, false, true, 128, (p.row + 15) & ~15);
-    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (leader) mma_commit(bar);
-    };
+    const bool per_map = p.maps() == 2;
+    const int steps_row = (p.row + 15) / 16;
     bool ok = true;
-    uint32_t g0 = 0, item = 0, sp0 = 0, sp1 = 0;
+    uint32_t item = 0, sp0 = 0, sp1 = 0;
+    uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // ring positions: slot and phase
     do {
       const int cnt = w.t1 - w.t0;
       const bool two = is_two();
       const int U = two ? 2 * cnt : cnt;
       auto issue_qk = [&](int u) -> bool {
         const int b = u & 1;
-        const uint32_t g = g0 + (two ? u >> 1 : u);
-        const int slot = g % NSK;
-        if ((!two || b == 0) && !wait_all(k_full + slot, (g / NSK) & 1, kDevTimeoutKFull)) return false;
+        if ((!two || b == 0) && !mbar_wait(k_full + ks, kp, status, kDevTimeoutKFull)) return false;
         // the buffer's previous P has been multiplied (before the item: q_full says so)
-        if (u >= 2 && !wait_all(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, kDevTimeoutODone)) return false;
+        if (u >= 2 && !mbar_wait(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, status, kDevTimeoutODone)) return false;
         tc_fence_after();
-        if (leader) {
-          // the columns that hold q: a row's, or its map's where a block is a map
-          const int lo = two && p.maps() == 2 ? b * p.dq / 16 : 0;
-          const int hi = (two && p.maps() == 2 ? (b + 1) * p.dq + 15 : p.row + 15) / 16;
-          const uint64_t a0 = dq + (two ? b * kQStep : 0), b0 = dk + slot * kStep;
-          for (int kk = lo; kk < hi; ++kk) {
-            const uint64_t in = (uint64_t)(kk % 4) * 32;
-            mma_ss(tmem + C::S_COL(b), a0 + (((kk / 4) * (128 * 128) + in) >> 4), b0 + (((kk / 4) * (TK * 128) + in) >> 4),
-                   kIdescQk, kk > lo, false);
+        // the columns that hold q: a row's, or its map's where a block is a map
+        const int lo = two && per_map ? b * p.dq / 16 : 0;
+        const int hi = two && per_map ? ((b + 1) * p.dq + 15) / 16 : steps_row;
+        const uint64_t a0 = dq + (two && b ? kQStep : 0), b0 = dk + ks * kStep;
+        const uint32_t d = tmem + C::S_COL(b);
+        auto step = [&](int kk) {
+          const uint32_t in = (kk % 4) * (32 >> 4);
+          mma_ss(d, a0 + ((kk / 4) * ((128 * 128) >> 4) + in), b0 + ((kk / 4) * ((TK * 128) >> 4) + in), kIdescQk, kk > lo, false);
+        };
+        // (one unrolled loop with a condition on each step gave products of the wrong operands with nvcc 12.9)
+        if (lo == 0 && hi == D / 16) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) step(kk);
+        } else {
+#pragma unroll 1
+          for (int kk = lo; kk < hi; ++kk) step(kk);
+        }
+        mma_commit(s_full + b);
+        if (!two || b == 1) {
+          mma_commit(k_empty + ks);
+          if (++ks == NSK) {
+            ks = 0;
+            kp ^= 1;
           }
         }
-        commit(s_full + b);
-        if (!two || b == 1) commit(k_empty + slot);
         return true;
       };
       // Q is written after the previous item's last product, so the S buffers and O are free from here on
-      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
+      ok = mbar_wait(q_full, item & 1, status, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
       for (int u = 0; u < U && ok; ++u) {
         const int b = u & 1;
-        const uint32_t g = g0 + (two ? u >> 1 : u), ph = (b ? sp1 : sp0) + (u >> 1);
-        const int slot = g % NSV;
-        const uint64_t v0 = dv + slot * kStep;
-        auto issue_pv = [&](int half) {
-          tc_fence_after();
-          if (leader) {
+        const uint32_t ph = ((b ? sp1 : sp0) + (u >> 1)) & 1;
+        const uint64_t v0 = dv + vs * kStep;
+        const uint32_t o = tmem + C::O_COL(b), pcol = tmem + C::S_COL(b);
+        ok = ((two && b == 1) || mbar_wait(v_full + vs, vp, status, kDevTimeoutVFull)) &&
+             mbar_wait(p_lo + b, ph, status, kDevTimeoutPFull);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-            for (int kk = half * (TK / 32); kk < (half + 1) * (TK / 32); ++kk)
-              mma_ts(tmem + C::O_COL(b), tmem + C::S_COL(b) + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv,
-                     (u >= NB || kk > 0) ? 1u : 0u, false);
+        for (int kk = 0; kk < TK / 32; ++kk)
+          mma_ts(o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u, false);
+        ok = mbar_wait(p_full + b, ph, status, kDevTimeoutPFull);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = TK / 32; kk < TK / 16; ++kk)
+          mma_ts(o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, 1u, false);
+        mma_commit(pv_done + b);
+        if (!two || b == 1) {
+          mma_commit(v_empty + vs);
+          if (++vs == NSV) {
+            vs = 0;
+            vp ^= 1;
           }
-        };
-        ok = (two && b == 1) || wait_all(v_full + slot, (g / NSV) & 1, kDevTimeoutVFull);
-        if (!ok || !(ok = wait_all(p_lo + b, ph & 1, kDevTimeoutPFull))) break;
-        issue_pv(0);
-        if (!(ok = wait_all(p_full + b, ph & 1, kDevTimeoutPFull))) break;
-        issue_pv(1);
-        if (!two || b == 1) commit(v_empty + slot);
-        commit(pv_done + b);
-        if (u + NB >= U) commit(o_done + (NB == 2 ? b : 0));
+        }
+        if (u + NB >= U) mma_commit(o_done + (NB == 2 ? b : 0));
         if (u + 2 < U) ok = issue_qk(u + 2);
       }
-      g0 += cnt;
       sp0 += (U + 1) >> 1;
       sp1 += U >> 1;
       ++item;
     } while (ok && w.next(p));
     // all tensor-core work this thread issued has finished before TMEM is released
-    commit(fin);
-    wait_all(fin, 0, kDevTimeoutFinal);
+    mma_commit(fin);
+    mbar_wait(fin, 0, status, kDevTimeoutFinal);
+    }
+    __syncwarp();
   } else if (warp < kWarpK) {
     // -------------------------------------------------------------- softmax and epilogue
     if constexpr (NB == 2) regs_increase<216>();
@@ -761,8 +448,6 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       const int cnt = w.t1 - w.t0, tokens = w.tokens(p);
       const bool two = is_two();
       const int steps = NB == 1 || two ? cnt : (cnt + 1 - blk) >> 1;  // this block's
-      const bool quarters = !two && tokens * group <= 32;
-      const bool carry = quarters && tokens * group <= 16;  // lanes 16..31 hold what rounding P drops
       const int off = w.s.kv - w.s.seq;
       // this thread's row: its token in the tile and query head
       int tok, qh;
@@ -772,10 +457,9 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         qh = (w.h * gh + r % gh) * 2 + blk;
         valid = tok < tokens;
       } else {
-        const int rr = quarters ? (carry ? lane & 15 : lane) : r;
-        tok = rr / group + (two ? blk * p.tb1 : 0);
-        qh = w.h * group + rr % group;
-        valid = tok < tokens && (!two || blk == 1 || rr / group < p.tb1);
+        tok = r / group + (two ? blk * p.tb1 : 0);
+        qh = w.h * group + r % group;
+        valid = tok < tokens && (!two || blk == 1 || r / group < p.tb1);
       }
       const int64_t token0 = w.cu + (int64_t)w.rt * p.tb, token = token0 + tok;
       RowState rs;
@@ -791,13 +475,21 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         const bool share = NB == 2 && !two;
         const uint32_t dst = smem_addr(sQ) + (two ? blk * C::Q_BYTES : 0) + r * 128;
         const int c0 = share ? blk * (D / 16) : 0;
+        constexpr int G = 8;  // 16-byte loads in flight
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          if (share && i >= D / 16) break;
-          const int c = c0 + i;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (c >= lo && c < hi) v = __ldg(src + (c - lo));
-          st_shared_v4(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4), v);
+        for (int i0 = 0; i0 < D / 8; i0 += G) {
+          if (share && i0 >= D / 16) break;
+          uint4 v[G];
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const int c = c0 + i0 + i;
+            v[i] = c >= lo && c < hi ? __ldg(src + (c - lo)) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const int c = c0 + i0 + i;
+            if (!share || i0 + i < D / 16) st_shared_v4(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4), v[i]);
+          }
         }
       }
       __syncwarp();
@@ -805,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       tc_fence_before();  // the previous item's loads of O come before the product that overwrites it
       mbar_arrive(q_full);
       // ---- key tiles, from the last
-      const bool warp_rows = quarters || __any_sync(0xffffffffu, valid);
+      const bool warp_rows = __any_sync(0xffffffffu, valid);
       for (int s = 0; s < steps && ok; ++s) {
         const int sb = NB == 2 ? blk : s & 1;  // S buffer
         const uint32_t ph = NB == 2 ? sp0 + s : (sb ? sp1 : sp0) + (s >> 1);
@@ -849,27 +541,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
           mbar_arrive(bar);
         };
         uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-        if (quarters) {
-          constexpr int NC = TK / 4;
-          float x[NC];
-          load_cols<NC>(s_col + wq * NC, x);
-          const float alpha = grow(rs, scores<NC>(p, rs, x, j0 + wq * NC, raw_max));
-          ok = rescale(alpha);
-          if (!ok) break;
-          const float base = rs.m == -INFINITY ? 0.f : rs.m;
-          uint32_t pk[NC / 2];
-          exponentials<T, NC>(x, scale2, f2pack(-base, -base), acc, pk, carry && lane >= 16);
-          store_p<NC / 2>(s_col + wq * (NC / 2), pk);
-          const uint32_t zero[NC / 2] = {};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q != wq) store_p<NC / 2>(s_col + q * (NC / 2), zero);
-          rs.l = rs.l * alpha + sum4(acc);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(p_lo + sb);
-          mbar_arrive(p_full + sb);
-        } else if (warp_rows) {
+        if (warp_rows) {
           // Half of the columns at a time, in 64 registers: the second half for its maximum, then the first for its
           // maximum and its P, then the second again (P goes over the first half's scores only).
           constexpr int NC = TK / 2;
@@ -884,12 +556,12 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
           const float base = rs.m == -INFINITY ? 0.f : rs.m;
           const uint64_t negm2 = f2pack(-base, -base);
           uint32_t pk[NC / 2];
-          exponentials<T, NC>(x, scale2, negm2, acc, pk, false);
+          exponentials<T, NC>(x, scale2, negm2, acc, pk);
           store_p<NC / 2>(s_col, pk);
           load_cols<NC>(s_col + NC, x);
           half_done(p_lo + sb);
           scores<NC>(p, rs, x, j0 + NC, raw_max);
-          exponentials<T, NC>(x, scale2, negm2, acc, pk, false);
+          exponentials<T, NC>(x, scale2, negm2, acc, pk);
           store_p<NC / 2>(s_col + NC / 2, pk);
           half_done(p_full + sb);
           rs.l = rs.l * alpha + sum4(acc);
@@ -929,142 +601,6 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         owner = true;
       }
       line += cnt;
-      if (quarters) {
-        // ---- join the lane quarters of the blocks: O = sum_w 2^(m_w - M) O_w, l alike.  All warps leave some of
-        // their columns at a time in the Q buffers (4 NB x 32 rows x COLS floats fill them), then every thread
-        // sums 8 columns of a row over the quarters.
-        constexpr int NP = NB * 4, COLS = C::SCRATCH / (NP * 32 * 4), PASSES = D / COLS;
-        constexpr int CH = COLS / 8;  // 8-column chunks of a row in a pass
-        constexpr int NK = CH * 32 > NB * 128 ? CH * 32 / (NB * 128) : 1;
-        constexpr int F4 = COLS / 4;
-        float4* scratch = reinterpret_cast<float4*>(sQ);
-        const int rows = tokens * group;
-        const int me = blk * 4 + wq;
-        sM[me * 32 + lane] = rs.m;
-        meet();
-        float top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < NP; ++q) top = fmaxf(top, sM[q * 32 + lane]);
-        const float f = fast_exp2(rs.m - (top == -INFINITY ? 0.f : top));
-        float y[NK][PASSES][8], sum[NK];
-#pragma unroll
-        for (int pass = 0; pass < PASSES; ++pass) {
-#pragma unroll 1
-          for (int c32 = 0; c32 < COLS / 32; ++c32) {
-            uint32_t regs[32];
-            if (steps > 0) {
-              tmem_ld32(o_col + pass * COLS + c32 * 32, regs);
-              tmem_ld_wait();
-            }
-            if (valid) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (steps > 0)
-                  v = make_float4(__uint_as_float(regs[4 * c]) * f, __uint_as_float(regs[4 * c + 1]) * f,
-                                  __uint_as_float(regs[4 * c + 2]) * f, __uint_as_float(regs[4 * c + 3]) * f);
-                scratch[(me * 32 + lane) * F4 + ((c32 * 8 + c) ^ (lane & 7))] = v;
-              }
-            }
-            __syncwarp();
-          }
-          if (pass == PASSES - 1) sM[me * 32 + lane] = rs.l * f;  // every warp has read the maxima
-          meet();
-#pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            const int chunk = threadIdx.x + k * NB * 128, row = chunk / CH, c8 = chunk % CH;
-            float(&a)[8] = y[k][pass];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = 0.f;
-            if (pass == PASSES - 1) sum[k] = 0.f;
-            if (row < rows) {
-#pragma unroll
-              for (int q = 0; q < NP; ++q) {
-#pragma unroll
-                for (int up = 0; up < 2; ++up) {
-                  if (up == 1 && !carry) continue;
-                  const int at = row + up * 16;
-#pragma unroll
-                  for (int h4 = 0; h4 < 2; ++h4) {
-                    const float4 v = scratch[(q * 32 + at) * F4 + ((c8 * 2 + h4) ^ (at & 7))];
-                    a[4 * h4] += v.x;
-                    a[4 * h4 + 1] += v.y;
-                    a[4 * h4 + 2] += v.z;
-                    a[4 * h4 + 3] += v.w;
-                  }
-                }
-                if (pass == PASSES - 1) sum[k] += sM[q * 32 + row];
-              }
-            }
-          }
-          meet();
-        }
-        // ---- and its epilogue
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const int chunk = threadIdx.x + k * NB * 128, row = chunk / CH, c8 = chunk % CH;
-          const float m = __shfl_sync(0xffffffffu, top, row & 31);
-          const bool mine = row < rows && ok;
-          if (!whole) {
-            if (mine) {
-              if (c8 == 0) p.ml[prow0 + row] = make_float2(m, sum[k]);
-#pragma unroll
-              for (int pass = 0; pass < PASSES; ++pass)
-                if (pass * COLS + c8 * 8 < p.row)
-                  st_global_v8(p.part + (prow0 + row) * D + pass * COLS + c8 * 8, reinterpret_cast<uint32_t*>(y[k][pass]));
-            }
-            continue;
-          }
-          const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;  // a row without keys gets 0
-          const int64_t t = token0 + row / group;
-          const int h = w.h * group + row % group;
-          float post = inv;
-          if (maps == 2) {
-            // rows 2i and 2i + 1 are the two maps of a head, CH lanes apart
-            const float wgt = !mine ? 0.f : (row & 1) ? -p.lambda[h >> 1] * inv : inv;
-            float ss = 0.f;
-#pragma unroll
-            for (int pass = 0; pass < PASSES; ++pass)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float v = y[k][pass][i] * wgt;
-                v += __shfl_xor_sync(0xffffffffu, v, CH);
-                if (pass * COLS + c8 * 8 >= p.row) v = 0.f;
-                y[k][pass][i] = v;
-                ss = fmaf(v, v, ss);
-              }
-            post = p.out_scale;
-            if (p.norm_weight) {
-#pragma unroll
-              for (int o = 1; o < CH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              post = p.out_scale * rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
-            }
-          }
-#pragma unroll
-          for (int pass = 0; pass < PASSES; ++pass) {
-            const int col = pass * COLS + c8 * 8;
-            // of the two lanes that hold a differential row, the even one stores the even passes
-            if (!mine || col >= p.row || (maps == 2 && (row & 1) != (pass & 1))) continue;
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float a = y[k][pass][2 * i] * post, b = y[k][pass][2 * i + 1] * post;
-              if (maps == 2 && p.norm_weight) {
-                a *= __ldg(p.norm_weight + col + 2 * i);
-                b *= __ldg(p.norm_weight + col + 2 * i + 1);
-              }
-              o[i] = pack2(a, b, (T*)nullptr);
-            }
-            st_global_v4(static_cast<T*>(p.out) + (t * (p.heads / maps) + h / maps) * p.row + col, o);
-          }
-          if (mine && p.lse && c8 == 0) {
-            float lse = sum[k] > 0.f ? m * kLn2 + logf(sum[k]) : -INFINITY;
-            if (p.mask_type == 5) lse += p.slopes[h] * static_cast<float>(w.rt * p.tb + row / group + off);
-            p.lse[t * p.heads + h] = lse;
-          }
-        }
-        continue;
-      }
       bool has_rows = warp_rows;
       float* exchange = reinterpret_cast<float*>(sQ);  // a row of XCOLS floats for each thread, chunks swizzled by the row
       constexpr int XCOLS = C::SCRATCH / (128 * 4) < D ? C::SCRATCH / (128 * 4) : D;
@@ -1409,9 +945,10 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Pa
 }
 
 template <typename T, int D>
-cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool two, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool few, bool two, cudaStream_t stream) {
   cudaError_t e;
-  if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
+  if (few) e = launch_paged_few(std::is_same_v<T, __half> ? kF16 : kBF16, D, tmK, tmV, p, stream);
+  else if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
   else if constexpr (D == 64) e = launch_attn<T, D, 2>(tmK, tmV, p, stream);
   else e = two ? launch_attn<T, D, 2>(tmK, tmV, p, stream) : launch_attn<T, D, 1>(tmK, tmV, p, stream);
   if (e != cudaSuccess) return e;
@@ -1495,19 +1032,20 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     p.tb1 = 128 / p.group;
     // Two blocks of rows where sequences have more than one block's on average (the lengths are on the device; any
     // lengths run on either); at D = 64 there is room for both Q blocks and deep rings anyway.
+    const bool few = p.group <= kFewRows && plan->n_tokens * p.group <= (int64_t)40 * p.batch;
     const bool two = D == 64 || (D == 128 && plan->n_tokens * p.group > (int64_t)128 * p.batch);
-    p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
+    p.tb = few ? kFewRows / p.group : !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
     p.box_rows = box;
     p.scale_log2 = plan->qk_scale * kLog2e;
     p.norm_eps = plan->norm_eps;
     p.out_scale = plan->out_scale;
     const bool f16 = plan->dtype == ALA_F16;
     if (D == 64)
-      e = f16 ? launch<__half, 64>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 64>(plan->tmK, plan->tmV, p, two, stream);
+      e = f16 ? launch<__half, 64>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 64>(plan->tmK, plan->tmV, p, few, two, stream);
     else if (D == 128)
-      e = f16 ? launch<__half, 128>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 128>(plan->tmK, plan->tmV, p, two, stream);
+      e = f16 ? launch<__half, 128>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 128>(plan->tmK, plan->tmV, p, few, two, stream);
     else
-      e = f16 ? launch<__half, 256>(plan->tmK, plan->tmV, p, two, stream) : launch<__nv_bfloat16, 256>(plan->tmK, plan->tmV, p, two, stream);
+      e = f16 ? launch<__half, 256>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 256>(plan->tmK, plan->tmV, p, few, two, stream);
   }
   if (e != cudaSuccess) {
     snprintf(err, errlen, "kernel launch failed: %s", cudaGetErrorString(e));

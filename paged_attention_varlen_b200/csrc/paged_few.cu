@@ -1,0 +1,648 @@
+// paged_few.cu -- paged attention where a kv head has few query rows: one token, or a few, of each sequence.
+//
+// With R rows (8, 16 or 32 that hold the item's) the products are taken transposed, so that the keys, of which
+// there are many, fill the 128 lanes of the tensor core, and the rows are its N:
+//   S^T [128 keys x R]  = K_tile [128 x d] Q^T
+//   O^T [d x N]        += V_tile^T [d x 128 keys] P^T
+// A thread owns a key and half of the rows: it takes R / 2 scores, and its part of their sums stays in registers
+// until the item ends, so a tile needs no reduction at all.  The running maxima are common to all threads and only
+// move when some score is more than 2^8 above its row's (one vote of the threads a tile; under ALiBi too, since
+// tiles run from the last key to the first, the largest scores first).  P goes to shared memory as the products' second operand.
+// With R <= 16 the N columns are 2 R: the second R carry what rounding P to 16 bits dropped, which makes P V exact
+// to 2^-17 or so at no cost (N is at least 16, and the products are a tenth of the time).
+//
+// It is bound by the cache's bytes: 48 cycles of tensor work and some 500 of softmax a tile of 128 keys, against
+// 2700 (d = 128) that the tile takes to arrive at a CTA's share of HBM.  What is left for speed is to keep loads
+// in flight, so the rest of shared memory is one ring of K and V tiles in the order of their use (192 KB: 4.2 us
+// of HBM at a CTA's share), which also covers the change from one item to the next.
+//
+// The line of tiles, its split over the CTAs and the partials of cut items are those of paged_attn.cu.
+//   warps 0..7  softmax (threads r and r + 128: key r of the tile, TMEM lane r, the first and the second half of
+//               the rows) and epilogue (column r of O)
+//   warp 8      TMA producer;  warp 9  tcgen05 issuer
+#include "paged_common.cuh"
+
+namespace ala {
+
+namespace {
+
+template <typename T, int D_>
+struct Few {
+  static constexpr int D = D_, TK = 128, CB = D / 64;
+  static constexpr int KV_BYTES = TK * D * 2;
+  static constexpr int NS = 192 * 1024 / KV_BYTES;  // ring slots
+  static constexpr int MT = D == 256 ? 2 : 1;       // 128-row tiles of O^T (D = 64: its upper lanes are not read)
+  static constexpr int QCB = kFewRows * 128;        // bytes of a 64-column block of Q
+  static constexpr int Q_BYTES = CB * QCB;
+  static constexpr int P_BYTES = 2 * QCB;           // [2 blocks of 64 keys][32 rows][128 B]
+  static constexpr int N_BARS = 1 + 2 * NS + 6 + 2;
+  static constexpr int THREADS = 320;
+  static constexpr int SMEM = 1024 + NS * KV_BYTES + Q_BYTES + 2 * P_BYTES + N_BARS * 8 + 16;
+  static constexpr uint32_t O_COL = 64, TMEM_COLS = 128;  // S^T [0, 32) and [32, 64), O^T from 64
+  static_assert(SMEM + 1400 <= 232448, "shared memory budget (1400: the static part)");
+};
+
+// What the threads share about an item's rows, and the scratch of their reductions.
+struct RowTables {
+  float slope_log2[kFewRows];  // of the row's head
+  int pos[kFewRows];           // position of the row's token
+  int last_key[kFewRows];      // keys up to this one are allowed (-1: none)
+  float m[kFewRows];
+  float red[4][kFewRows];      // per lane quarter
+};
+
+__device__ __forceinline__ bool any_of_256(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 2, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// N columns of 32-bit values from TMEM column `col` on (no wait)
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t col, uint32_t (&r)[N]) {
+  if constexpr (N == 4) tmem_ld4(col, r);
+  else if constexpr (N == 8) tmem_ld8(col, r);
+  else tmem_ld16(col, r);
+}
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t col, const uint32_t (&r)[N]) {
+  if constexpr (N == 4) tmem_st4(col, r);
+  else if constexpr (N == 8) tmem_st8(col, r);
+  else tmem_st16(col, r);
+}
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+
+// Where the softmax warps are.
+struct FewState {
+  uint32_t g;     // steps so far (buffer g & 1, phase g / 2)
+  uint32_t item;  // items so far
+  bool ok;
+};
+
+constexpr float kNoKey = -3.0e38f;
+
+// One item: its key tiles and its epilogue, R rows, RT of them this thread's.  After a failed wait a warp skips the waits that are left, but
+// goes through every tile and item, so that the warps meet as often as ever.
+template <typename T, int D, int R>
+__device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>& w, FewState& f, RowTables& tab, uint8_t* sVring,
+                                         uint32_t v_slot0, uint64_t* v_full0, uint32_t v_phase0, uint32_t sP, uint64_t* s_full,
+                                         uint64_t* p_full, uint64_t* pv_done, uint64_t* o_done, uint32_t tmem, int64_t token0,
+                                         int tokens) {
+  using C = Few<T, D>;
+  constexpr bool kCarry = R <= 16;
+  constexpr int RT = R / 2;
+  const int r = threadIdx.x & 127, quarter = r >> 5, lane = r & 31;
+  const int n0 = (threadIdx.x >> 7) * RT;  // this thread's rows: n0 .. n0 + RT - 1
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  const int group = p.group, rows = tokens * group, mt = p.mask_type, maps = p.maps();
+  const bool alibi = mt == 3 || mt == 4 || mt == 5;
+  const float scale = p.scale_log2;
+  int* status = p.status;
+  const int first_last = tab.last_key[0];  // the earliest token sees fewest keys
+  // Maxima in log2 units (the ones P is computed against) and sums.  A row that has met no key has a maximum below
+  // any score, and finite, so that it needs no case of its own.
+  float m[RT], l[RT];
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    m[n] = kNoKey;
+    l[n] = 0.f;
+  }
+  // this key's place in a row of P: [block of 64 keys][row][128 B], 16-byte chunks swizzled by the row
+  const uint32_t pk0 = (r >> 6) * C::QCB + (r & 7) * 2, pchunk = (r & 63) >> 3;
+  const int cnt = w.t1 - w.t0;
+  for (int u = 0; u < cnt; ++u, ++f.g) {
+    const int j0 = (w.t1 - 1 - u) * 128, key = j0 + r;
+    const int b = f.g & 1;
+    if (f.ok) f.ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (f.g >> 1) & 1, status, kDevTimeoutSFull));
+    tc_fence_after();
+    uint32_t raw[RT];
+    ld_cols<RT>(tmem + lanes + b * 32 + n0, raw);
+    tmem_ld_wait();
+    float t[RT];
+#pragma unroll
+    for (int n = 0; n < RT; ++n) t[n] = __uint_as_float(raw[n]) * scale;
+    if (alibi) {
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        // right- and left-aligned bias differ by a per-row constant; both use (key - pos)
+        const float ahead = static_cast<float>(key - tab.pos[n0 + n]), s = tab.slope_log2[n0 + n];
+        t[n] = mt == 4 ? fmaf(-s, sqrt_approx(fmaxf(-ahead, 0.f)), t[n]) : fmaf(s, ahead, t[n]);
+      }
+    }
+    if (j0 + 127 > first_last) {
+#pragma unroll
+      for (int n = 0; n < RT; ++n) t[n] = key > tab.last_key[n0 + n] ? -INFINITY : t[n];
+    }
+    float over = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < RT; n += 2) over = max3(over, t[n] - m[n], t[n + 1] - m[n + 1]);
+    if (any_of_256(over > kRescaleThreshold)) {
+      // some row's maximum moves: every row takes its tile's
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        float v = t[n];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (lane == 0) tab.red[quarter][n0 + n] = v;
+      }
+      named_barrier_sync(1, 256);
+      float alpha[RT];
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        const float top = fmaxf(fmaxf(tab.red[0][n0 + n], tab.red[1][n0 + n]), fmaxf(tab.red[2][n0 + n], tab.red[3][n0 + n]));
+        const float m_new = fmaxf(m[n], top);
+        alpha[n] = fast_exp2(m[n] - m_new);
+        m[n] = m_new;
+        l[n] *= alpha[n];
+      }
+      if (u > 0) {
+        if (f.ok)
+          f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (b ^ 1), ((f.g - 1) >> 1) & 1, status, kDevTimeoutODone));
+        tc_fence_after();
+#pragma unroll
+        for (int mi = 0; mi < C::MT; ++mi)
+#pragma unroll
+          for (int part = 0; part < (kCarry ? 2 : 1); ++part) {
+            const uint32_t col = tmem + lanes + C::O_COL + mi * 32 + part * R + n0;
+            uint32_t o[RT];
+            ld_cols<RT>(col, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int n = 0; n < RT; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
+            st_cols<RT>(col, o);
+          }
+        tmem_st_wait();
+      }
+    }
+    // P: rounded to the operands' 16 bits; the sums take the unrounded values, so a row's rounding errors average
+    // out instead of biasing its normalisation
+    uint32_t hi[RT / 2], lo[RT / 2];
+#pragma unroll
+    for (int n = 0; n < RT; n += 2) {
+      const float e0 = fast_exp2(t[n] - m[n]), e1 = fast_exp2(t[n + 1] - m[n + 1]);
+      l[n] += e0;
+      l[n + 1] += e1;
+      hi[n / 2] = pack2(e0, e1, (T*)nullptr);
+      if constexpr (kCarry) {
+        const float2 h = unpack2(hi[n / 2], (T*)nullptr);
+        lo[n / 2] = pack2(e0 - h.x, e1 - h.y, (T*)nullptr);
+      }
+    }
+    // the buffer's previous P has been multiplied
+    if (u >= 2 && f.ok)
+      f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + b, ((f.g >> 1) - 1) & 1, status, kDevTimeoutODone));
+    const uint32_t prow = sP + b * C::P_BYTES + pk0 + n0 * 128;
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      const uint32_t at = prow + n * 128 + ((pchunk ^ ((n0 + n) & 7)) << 4);
+      st_shared_u16(at, (n & 1) ? hi[n / 2] >> 16 : hi[n / 2]);
+      if constexpr (kCarry) st_shared_u16(at + R * 128, (n & 1) ? lo[n / 2] >> 16 : lo[n / 2]);  // R is a multiple of 8
+    }
+    if (u == 0 && j0 + 128 > w.s.kv) {
+      // slots past kvSeqLen may hold anything, NaN included, and 0 * NaN is not 0: clear their V rows
+      if (f.ok) f.ok = __all_sync(0xffffffffu, mbar_wait(v_full0, v_phase0, status, kDevTimeoutVFull));
+      if (threadIdx.x < 128 && key >= w.s.kv && f.ok) {
+        const uint32_t dst = smem_addr(sVring + v_slot0 * C::KV_BYTES) + r * 128;
+#pragma unroll
+        for (int cb = 0; cb < C::CB; ++cb)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) st_shared_v4(dst + cb * (128 * 128) + c * 16, make_uint4(0, 0, 0, 0));
+      }
+      __syncwarp();
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    mbar_arrive(p_full + b);
+  }
+  // ---- the sums of all keys, and O
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
+  }
+  if (f.ok) f.ok = __all_sync(0xffffffffu, mbar_wait(o_done, f.item & 1, status, kDevTimeoutODone));
+  ++f.item;
+  tc_fence_after();
+  // every thread has left the last tile, so what it shared there has been read
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    if (lane == 0) tab.red[quarter][n0 + n] = l[n];
+    if (r == 0) tab.m[n0 + n] = m[n];
+  }
+  named_barrier_sync(1, 256);
+  const bool whole = w.t0 == 0 && w.t1 == w.n;
+  const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * (D == 256 ? 128 : 256);
+  auto total = [&](int n) { return (tab.red[0][n] + tab.red[1][n]) + (tab.red[2][n] + tab.red[3][n]); };
+  if (threadIdx.x < rows && f.ok) {  // thread n: row n's statistics
+    const int n = threadIdx.x;
+    const float sum = total(n), top = tab.m[n];
+    if (!whole) {
+      p.ml[prow0 + n] = make_float2(top, sum);
+    } else if (p.lse) {
+      const int h = w.h * group + n % group;
+      float lse = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+      if (mt == 5) lse += p.slopes[h] * static_cast<float>(tab.pos[n]);  // left-aligned = right-aligned + slope * position
+      p.lse[(token0 + n / group) * p.heads + h] = lse;
+    }
+  }
+  float o[C::MT][RT];  // column r (+ 128) of this thread's rows
+#pragma unroll
+  for (int mi = 0; mi < C::MT; ++mi) {
+    uint32_t raw[RT], rest[RT];
+    const uint32_t col = tmem + lanes + C::O_COL + mi * 32 + n0;
+    ld_cols<RT>(col, raw);
+    if constexpr (kCarry) ld_cols<RT>(col + R, rest);
+    tmem_ld_wait();
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      o[mi][n] = __uint_as_float(raw[n]);
+      if constexpr (kCarry) o[mi][n] += __uint_as_float(rest[n]);
+    }
+  }
+  if (!whole) {
+#pragma unroll
+    for (int mi = 0; mi < C::MT; ++mi) {
+      const int col = mi * 128 + r;
+      if (col >= p.row || !f.ok) continue;
+      float* dst = p.part + (prow0 + n0) * D + col;
+#pragma unroll
+      for (int n = 0; n < RT; ++n)
+        if (n0 + n < rows) dst[(int64_t)n * D] = o[mi][n];
+    }
+  } else if (maps == 1) {
+    // the rows of one token follow each other; the next token's lie p.heads rows on
+    int hh = n0 % group;
+    T* dst = static_cast<T*>(p.out) + ((token0 + n0 / group) * p.heads + w.h * group + hh) * p.row + r;
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      if (n0 + n < rows) {
+        const float sum = total(n0 + n), inv = sum > 0.f ? 1.f / sum : 0.f;  // a row without keys gets 0
+#pragma unroll
+        for (int mi = 0; mi < C::MT; ++mi)
+          if (mi * 128 + r < p.row && f.ok) dst[mi * 128] = from_float<T>(o[mi][n] * inv);
+        dst += p.row;
+        if (++hh == group) {
+          hh = 0;
+          dst += (int64_t)(p.heads - group) * p.row;
+        }
+      }
+    }
+  } else {
+    // rows 2i and 2i + 1 are the two maps of a head
+    const int gh = group / 2, i0 = n0 / 2, outs = rows / 2;
+#pragma unroll
+    for (int i = 0; i < RT / 2; ++i) {
+      if (i0 + i < outs) {
+        const float s1 = total(n0 + 2 * i), s2 = total(n0 + 2 * i + 1);
+        const float w1 = s1 > 0.f ? 1.f / s1 : 0.f, w2 = s2 > 0.f ? -__ldg(p.lambda + w.h * gh + (i0 + i) % gh) / s2 : 0.f;
+#pragma unroll
+        for (int mi = 0; mi < C::MT; ++mi)
+          o[mi][i] = mi * 128 + r < p.row ? fmaf(o[mi][2 * i], w1, o[mi][2 * i + 1] * w2) : 0.f;
+      }
+    }
+    if (p.norm_weight) {
+      named_barrier_sync(1, 256);  // the sums have been read
+#pragma unroll
+      for (int i = 0; i < RT / 2; ++i) {
+        if (i0 + i < outs) {
+          float ss = 0.f;
+#pragma unroll
+          for (int mi = 0; mi < C::MT; ++mi) ss = fmaf(o[mi][i], o[mi][i], ss);
+#pragma unroll
+          for (int x = 16; x; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+          if (lane == 0) tab.red[quarter][i0 + i] = ss;
+        }
+      }
+      named_barrier_sync(1, 256);
+    }
+    int hh = i0 % gh;
+    T* dst = static_cast<T*>(p.out) + ((token0 + i0 / gh) * (p.heads / 2) + w.h * gh + hh) * p.row + r;
+#pragma unroll
+    for (int i = 0; i < RT / 2; ++i) {
+      if (i0 + i < outs) {
+        float post = p.out_scale;
+        if (p.norm_weight) post *= rsqrtf(total(i0 + i) / static_cast<float>(p.row) + p.norm_eps);
+#pragma unroll
+        for (int mi = 0; mi < C::MT; ++mi) {
+          const int col = mi * 128 + r;
+          if (col < p.row && f.ok)
+            dst[mi * 128] = from_float<T>(o[mi][i] * post * (p.norm_weight ? __ldg(p.norm_weight + col) : 1.f));
+        }
+        dst += p.row;
+        if (++hh == gh) {
+          hh = 0;
+          dst += (int64_t)(p.heads / 2 - gh) * p.row;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using C = Few<T, D>;
+  constexpr int NS = C::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem;                            // [NS][KV_BYTES]: K(0), K(1), V(0), K(2), V(1), ... of each item
+  uint8_t* sQ = ring + NS * C::KV_BYTES;           // [CB][32 rows][128 B]
+  uint8_t* sP = sQ + C::Q_BYTES;                   // [2][P_BYTES]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sP + 2 * C::P_BYTES);
+  uint64_t* q_full = bars;
+  uint64_t* full = bars + 1;
+  uint64_t* empty = full + NS;
+  uint64_t* s_full = empty + NS;    // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* pv_done = p_full + 2;   // [2]
+  uint64_t* o_done = pv_done + 2;
+  uint64_t* fin = o_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
+  __shared__ Start st;
+  __shared__ int64_t red[2 * C::THREADS / 32];
+  __shared__ RowTables tab;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  int* status = p.status;
+  constexpr int kWarpLoad = 8, kWarpMma = 9;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 256);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full + s, 1);
+      mbar_init(p_full + s, 256);
+      mbar_init(pv_done + s, 1);
+    }
+    mbar_init(o_done, 1);
+    mbar_init(fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  find_start<128, C::THREADS>(p, &st, red);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (st.b < 0) {  // fewer tiles than CTAs
+    if (threadIdx.x == 0) p.desc[blockIdx.x].n_seg = 0;
+    if (warp == kWarpMma) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
+  Walker<128> w;
+  w.b = st.b;
+  w.h = st.h;
+  w.rt = st.rt;
+  w.t0 = st.t0;
+  w.raw = st.raw;
+  w.cu = st.cu;
+  w.left = st.left;
+  w.s = st.s;
+  w.fetch(p);
+  w.enter(p);
+
+  // Barrier phases run on across items: the ring by a slot and its phase, the S and P buffers by a counter of tiles
+  // (buffer g & 1, phase g / 2), q_full and o_done by items.
+  if (warp == kWarpLoad) {
+    // -------------------------------------------------------------- producer: lane i loads box i of each tile
+    const bool leader = elect_one();
+    if (leader) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int bs = p.block_size, box = p.box_rows;
+    const bool has_box = lane * box < 128;
+    const int oob_row = p.num_blocks * bs;
+    bool ok = true;
+    uint32_t g = 0;  // loads so far
+    auto load = [&](const CUtensorMap* map, int row) {
+      const int slot = g % NS;
+      if (ok && g >= (uint32_t)NS)
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + slot, ((g / NS) - 1) & 1, status, kDevTimeoutKEmpty));
+      if (!ok) return;
+      if (leader) mbar_expect_tx(full + slot, C::KV_BYTES);
+      __syncwarp();
+      if (has_box) {
+        uint8_t* dst = ring + slot * C::KV_BYTES + lane * box * 128;
+#pragma unroll
+        for (int cb = 0; cb < C::CB; ++cb) tma_load_3d(dst + cb * (128 * 128), map, full + slot, cb * 64, w.h, row);
+      }
+      __syncwarp();
+      ++g;
+    };
+    do {
+      const int32_t* bt = p.block_tables + (size_t)w.b * p.max_blocks;
+      const int pages = (w.s.kv + bs - 1) / bs;
+      // the table entry of a tile's box is fetched one tile ahead, so its latency is not in the loop
+      int pg = ((w.t1 - 1) * 128 + lane * box) / bs;
+      int blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
+      int row_v = 0;
+      for (int j = w.t1 - 1; j >= w.t0; --j) {
+        const int pos = j * 128 + lane * box;
+        int row = oob_row;  // past the last page: the load fills zeros
+        if (has_box && pg < pages) {
+          if (blk >= 0 && blk < p.num_blocks) row = blk * bs + (pos - pg * bs);
+          else atomicCAS(status + 1, 0, kDevBadBlockIndex);
+        }
+        if (j > w.t0) {
+          pg = (pos - 128) / bs;
+          blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
+        }
+        load(&tmK, row);
+        if (j < w.t1 - 1) load(&tmV, row_v);
+        row_v = row;
+      }
+      load(&tmV, row_v);
+    } while (ok && w.next(p));
+    // never leave the CTA while loads this warp issued are still landing in shared memory
+    for (uint32_t i = g >= (uint32_t)NS ? g - NS : 0; i < g; ++i) mbar_wait(full + (i % NS), (i / NS) & 1, status, kDevTimeoutKFull);
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // -------------------------------------------------------------- MMA issuer: warp-uniform, one lane issues
+    const bool leader = elect_one();
+    const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_addr(ring), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(ring), 128 * 128, 1024);  // V^T: the columns run along M
+    const uint64_t dp = smem_desc_sw128(smem_addr(sP), 16, 1024);
+    constexpr uint64_t kStep = C::KV_BYTES >> 4, kPStep = C::P_BYTES >> 4;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
+    };
+    uint32_t slot = 0, phase = 0;
+    auto advance = [&]() {
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    bool ok = true;
+    uint32_t g = 0, item = 0;
+    do {
+      const int cnt = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      const int rows = __shfl_sync(0xffffffffu, w.tokens(p) * p.group, 0);
+      const uint32_t idesc_qk = instr_desc(ElemFmt<T>::fmt, false, false, 128, rows <= 16 ? 16 : 32);
+      const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, true, false, 128, rows <= 8 ? 16 : 32);
+      auto issue_qk = [&](uint32_t b) -> bool {
+        if (!wait_all(full + slot, phase, kDevTimeoutKFull)) return false;
+        tc_fence_after();
+        const uint64_t a0 = dk + slot * kStep;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + b * 32, a0 + (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2, dq + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2,
+                   idesc_qk, kk > 0, false);
+          mma_commit(s_full + b);
+          mma_commit(empty + slot);
+        }
+        __syncwarp();
+        advance();
+        return true;
+      };
+      // Q is written after the previous item's last product, so the S buffers and O are free from here on
+      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(g & 1);
+      for (int u = 0; u < cnt && ok; ++u, ++g) {
+        const uint32_t b = g & 1;
+        // S of the next tile goes over that of the last one, which has been read: its P has come
+        if (u + 1 < cnt && !(ok = issue_qk(b ^ 1))) break;
+        ok = wait_all(full + slot, phase, kDevTimeoutVFull) && wait_all(p_full + b, (g >> 1) & 1, kDevTimeoutPFull);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a0 = dv + slot * kStep, b0 = dp + b * kPStep;
+        if (leader) {
+#pragma unroll
+          for (int mi = 0; mi < C::MT; ++mi)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ss(tmem + C::O_COL + mi * 32, a0 + mi * ((2 * 128 * 128) >> 4) + kk * ((16 * 128) >> 4),
+                     b0 + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2, idesc_pv, (u > 0 || kk > 0) ? 1u : 0u, false);
+          mma_commit(empty + slot);
+          mma_commit(pv_done + b);
+          if (u == cnt - 1) mma_commit(o_done);
+        }
+        __syncwarp();
+        advance();
+      }
+      ++item;
+    } while (ok && w.next(p));
+    // all tensor-core work this warp issued has finished before TMEM is released
+    if (leader) mma_commit(fin);
+    __syncwarp();
+    wait_all(fin, 0, kDevTimeoutFinal);
+  } else {
+    // -------------------------------------------------------------- softmax and epilogue
+    const int r = threadIdx.x;
+    const int group = p.group, maps = p.maps();
+    FewState f{0, 0, true};
+    uint32_t loads = 0;  // ring slots used so far
+    bool owner = false;
+    int64_t line = st.line;
+    do {
+      const int tokens = w.tokens(p), rows = tokens * group, cnt = w.t1 - w.t0;
+      const int64_t token0 = w.cu + (int64_t)w.rt * p.tb;
+      const int off = w.s.kv - w.s.seq;
+      const int R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+      named_barrier_sync(1, 256);  // the last item's tables have been read
+      if (r < R) {
+        const int pos = w.rt * p.tb + r / group + off;
+        tab.pos[r] = pos;
+        // rows that fill up R see every key, so that they never decide whether a tile needs masks
+        tab.last_key[r] = p.mask_type == 0 || r >= rows ? w.s.kv - 1 : min(pos, w.s.kv - 1);
+        tab.slope_log2[r] = p.slopes && r < rows ? p.slopes[w.h * group + r % group] * kLog2e : 0.f;
+      }
+      // ---- Q, K-major with the 128-byte swizzle, zeros in the rows that fill up R and behind the row's columns
+      for (int i = r; i < R * (D / 8); i += 256) {
+        const int row = i / (D / 8), c = i % (D / 8);
+        const int qh = w.h * group + row % group;
+        const int lo = maps == 2 ? (qh & 1) * (p.dq / 8) : 0;  // map 2 in the upper half
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows && c >= lo && c < lo + p.dq / 8)
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (token0 + row / group) * p.q_stride + (int64_t)qh * p.dq) + (c - lo));
+        st_shared_v4(smem_addr(sQ) + (c >> 3) * C::QCB + row * 128 + (((c & 7) ^ (row & 7)) << 4), v);
+      }
+      __syncwarp();
+      fence_proxy_async_smem();
+      tc_fence_before();  // the previous item's loads of O come before the product that overwrites it
+      mbar_arrive(q_full);
+      named_barrier_sync(1, 256);  // the tables are written
+      const uint32_t v0 = loads + (cnt > 1 ? 2 : 1);  // the first tile's V in the order of loads
+      uint64_t* v_full0 = full + v0 % NS;
+      const uint32_t v_phase0 = (v0 / NS) & 1;
+      if (w.t0 == 0 && w.t1 < w.n && r == 0) {
+        // a cut item starts here; the last CTA c with c * total / ctas <= last tile
+        const int64_t last = line + w.n - 1;
+        PagedDesc d;
+        d.n_seg = (int)(((last + 1) * st.ctas - 1) / st.total) - (int)blockIdx.x + 1;
+        d.token0 = (int)token0;
+        d.tokens = tokens;
+        d.kv_head = w.h;
+        d.pos0 = w.rt * p.tb + off;
+        d.two = 0;
+        p.desc[blockIdx.x] = d;
+        owner = true;
+      }
+      const uint32_t sp = smem_addr(sP);
+      if (R == 8)
+        few_item<T, D, 8>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+      else if (R == 16)
+        few_item<T, D, 16>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+      else
+        few_item<T, D, 32>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+      loads += 2 * cnt;
+      line += cnt;
+    } while (w.next(p));
+    if (r == 0 && !owner) p.desc[blockIdx.x].n_seg = 0;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, cudaStream_t stream) {
+  using C = Few<T, D>;
+  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  paged_few_kernel<T, D><<<kGrid, C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_few(int32_t dtype, int D, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p,
+                             cudaStream_t stream) {
+  if (dtype == kF16)
+    return D == 64 ? launch<__half, 64>(tmK, tmV, p, stream)
+         : D == 128 ? launch<__half, 128>(tmK, tmV, p, stream) : launch<__half, 256>(tmK, tmV, p, stream);
+  return D == 64 ? launch<__nv_bfloat16, 64>(tmK, tmV, p, stream)
+       : D == 128 ? launch<__nv_bfloat16, 128>(tmK, tmV, p, stream) : launch<__nv_bfloat16, 256>(tmK, tmV, p, stream);
+}
+
+}  // namespace ala

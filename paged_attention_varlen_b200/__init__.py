@@ -362,14 +362,25 @@ def _same_device(first, **tensors):
             raise ValueError(f"{name} is on {x.device}, not on {first.device}")
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current; raises the library's error."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(call(s.cuda_stream))
+def _index(device) -> int:
+    """CUDA ordinal of ``device``; -1 for a device that nothing can be launched on."""
+    if device.type != "cuda":
+        return -1
+    return device.index if device.index is not None else torch.cuda.current_device()
+
+
+def _launch(index, stream, function, args):
+    """function(*args, stream handle) with device ``index`` current; raises the library's error."""
+    # the raw handle of the current stream: torch.cuda.current_stream builds a Stream object first, which costs a
+    # small call as much as its launch
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        status = function(*args, s)
     else:
-        _check(call(s.cuda_stream))
+        with torch.cuda.device(index):
+            status = function(*args, s)
+    if status != 0:
+        _check(status)
 
 
 def _capturing(stream) -> bool:
@@ -383,13 +394,17 @@ class PagedOp(Op):
     """A planned paged attention call.  Its first execution binds the workspace (a synchronisation), unless the
     stream is being captured; a captured execution needs no binding."""
 
+    def __init__(self, handle, ws_size, execute_fn, device, keep):
+        super().__init__(handle, ws_size, execute_fn, device, keep)
+        self._index = _index(device)
+        self._args = (self.workspace.data_ptr(), self.workspace_size, self._handle)
+
     def __call__(self, stream: torch.cuda.Stream | None = None):
         if not self._bound and not _capturing(stream):
-            _launch(self.workspace.device, stream, lambda s: lib().ala_op_bind_workspace(
-                self._handle, self.workspace.data_ptr(), self.workspace_size, s))
+            _launch(self._index, stream, lib().ala_op_bind_workspace,
+                    (self._handle, self.workspace.data_ptr(), self.workspace_size))
             self._bound = True
-        _launch(self.workspace.device, stream,
-                lambda s: self._execute(self.workspace.data_ptr(), self.workspace_size, self._handle, s))
+        _launch(self._index, stream, self._execute, self._args)
         return self
 
 
@@ -397,10 +412,10 @@ class PagedCall:
     """A planned call that needs no workspace: call it to run on the current stream."""
 
     def __init__(self, function, args, device, keep):
-        self._function, self._args, self._device, self._keep = function, args, device, keep
+        self._function, self._args, self._index, self._keep = function, args, _index(device), keep
 
     def __call__(self, stream: torch.cuda.Stream | None = None):
-        _launch(self._device, stream, lambda s: self._function(*self._args, s))
+        _launch(self._index, stream, self._function, self._args)
         return self
 
 

@@ -21,7 +21,7 @@ namespace {
 // between them, pushes before pops and reads of the inputs before writes of outputs that may be the same
 // memory, is a cluster barrier, so a step is one launch.
 constexpr int kStepThreads = 1024;
-constexpr int kStepCluster = 8;
+constexpr int kStepCluster = 16;
 
 struct StepRow {
   int cu, taken, given, before;  // sums over earlier rows, and this row's keys cached before
@@ -31,16 +31,37 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Both kernels are programmatic dependent launches: their blocks are scheduled while the kernel before them on the
+// stream ends, and wait here until it has completed.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A warp moves n block numbers, eight loads in flight in each lane: a request of 12000 keys holds 750 blocks of 16.
+template <class Load, class Store>
+__device__ __forceinline__ void move_blocks(int n, int lane, Load load, Store store) {
+  constexpr int U = 8;
+  for (int i0 = lane; i0 < n; i0 += 32 * U) {
+    int blk[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + 32 * u < n) blk[u] = load(i0 + 32 * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + 32 * u < n) store(i0 + 32 * u, blk[u]);
+  }
+}
+
 __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const PagedStepArgs a) {
   extern __shared__ StepRow rows[];  // [batch + 1]
   __shared__ int64_t warp_sum[3][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int bs = a.block_size;
   const int64_t room = (int64_t)a.max_blocks * bs;
-  const int per = (a.batch + kStepThreads - 1) / kStepThreads;
+  const int per = (a.batch + threads - 1) / threads;
   const int first = min(tid * per, a.batch), last = min(first + per, a.batch);
-  const int count = __ldg(a.free_count);
-  auto blocks_of = [&](int keys) { return (int)(((int64_t)keys + bs - 1) / bs); };
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.slot_mapping) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+  dependency_wait();  // of what comes before on the stream; nothing was read until here
+  const int count = *a.free_count;
+  auto blocks_of = [&](int keys) { return (int)(((unsigned)keys + (unsigned)bs - 1) / (unsigned)bs); };  // keys <= 2^30
 
   // ---- this thread's rows: their sums, and whether a length is out of range
   int64_t sum[3] = {0, 0, 0};
@@ -72,7 +93,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
   int64_t total[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const int64_t mine = warp_sum[i][lane];
+    const int64_t mine = lane < threads / 32 ? warp_sum[i][lane] : 0;
     int64_t before = lane < warp ? mine : 0, all = mine;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -89,7 +110,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
                                                                       : 0;
   if (code != 0) {  // the same for every CTA: the step changes nothing
     cluster_sync();  // every CTA has read its inputs
-    const int t0 = blockIdx.x * kStepThreads + tid, stride = gridDim.x * kStepThreads;
+    const int t0 = blockIdx.x * threads + tid, stride = gridDim.x * threads;
     for (int b = t0; b < a.batch; b += stride)
       if (a.kv_seq_len != a.context_len) a.kv_seq_len[b] = a.context_len[b];
     for (int b = t0; b <= a.batch; b += stride) a.cu_seq_len[b] = 0;
@@ -119,17 +140,17 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
   __syncthreads();
 
   // ---- blocks of ended requests onto the stack, one warp per row
-  const int warps = gridDim.x * (kStepThreads / 32), w0 = blockIdx.x * (kStepThreads / 32) + warp;
+  const int warps = gridDim.x * (threads / 32), w0 = blockIdx.x * (threads / 32) + warp;
   bool bad_block = false;
   if (total[2] > 0) {
     for (int b = w0; b < a.batch; b += warps) {
       const int at = count + rows[b].given, n = rows[b + 1].given - rows[b].given;
       const int32_t* row = a.block_tables + (int64_t)b * a.max_blocks;
-      for (int i = lane; i < n; i += 32) {
-        const int blk = row[i];
-        bad_block |= blk < 0 || blk >= a.capacity;
-        a.free_blocks[at + i] = blk;
-      }
+      move_blocks(n, lane, [&](int i) { return row[i]; },
+                  [&](int i, int blk) {
+                    bad_block |= blk < 0 || blk >= a.capacity;
+                    a.free_blocks[at + i] = blk;
+                  });
     }
   }
   // one thread clears the status before any CTA may report into it
@@ -142,11 +163,11 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
     const StepRow r = rows[b];
     const int n = rows[b + 1].taken - r.taken, have = blocks_of(r.before);
     int32_t* row = a.block_tables + (int64_t)b * a.max_blocks;
-    for (int i = lane; i < n; i += 32) {
-      const int blk = __ldcg(a.free_blocks + (top - 1 - r.taken - i));
-      bad_block |= blk < 0 || blk >= a.capacity;
-      row[have + i] = blk;
-    }
+    move_blocks(n, lane, [&](int i) { return __ldcg(a.free_blocks + (top - 1 - r.taken - i)); },
+                [&](int i, int blk) {
+                  bad_block |= blk < 0 || blk >= a.capacity;
+                  row[have + i] = blk;
+                });
     if (lane == 0) {
       a.kv_seq_len[b] = r.before + (rows[b + 1].cu - r.cu);
       a.cu_seq_len[b] = r.cu;
@@ -156,27 +177,44 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
     a.cu_seq_len[a.batch] = (int)total[0];
     *a.free_count_out = top - (int)total[1];
   }
-  // ---- slot and position of every token; a page that a row already had is in its table, a new one is still
-  // on the stack's top (nothing is written over it here)
-  for (int t = blockIdx.x * kStepThreads + tid; t < a.n_tokens; t += gridDim.x * kStepThreads) {
-    int slot = -1, pos = 0;
-    if (t < total[0]) {
-      int lo = 0, hi = a.batch;  // the last row with cu <= t
+  // ---- slot and position of every token, four at a time (one search, loads in flight together); a page that a row
+  // already had is in its table, a new one is still on the stack's top (nothing is written over it here)
+  for (int t0 = 4 * (blockIdx.x * threads + tid); t0 < a.n_tokens; t0 += 4 * gridDim.x * threads) {
+    int slot[4], pos[4];
+    int lo = 0, hi = a.batch;  // the last row with cu <= t0
+    if (t0 < total[0])
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (rows[mid].cu <= t) lo = mid;
+        if (rows[mid].cu <= t0) lo = mid;
         else hi = mid;
       }
-      const StepRow r = rows[lo];
-      pos = r.before + t - r.cu;
-      const int page = pos / bs, have = blocks_of(r.before);
-      const int blk = page < have ? a.block_tables[(int64_t)lo * a.max_blocks + page]
-                                  : __ldcg(a.free_blocks + (top - 1 - r.taken - (page - have)));
-      if (blk >= 0 && blk < a.capacity) slot = blk * bs + pos - page * bs;
-      else bad_block = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + i;
+      slot[i] = -1;
+      pos[i] = 0;
+      if (t < total[0]) {
+        while (rows[lo + 1].cu <= t) ++lo;  // ends at the last row: rows[batch].cu is the total
+        const StepRow r = rows[lo];
+        pos[i] = r.before + t - r.cu;
+        const int page = (unsigned)pos[i] / (unsigned)bs, have = blocks_of(r.before);
+        const int blk = page < have ? a.block_tables[(int64_t)lo * a.max_blocks + page]
+                                    : __ldcg(a.free_blocks + (top - 1 - r.taken - (page - have)));
+        if (blk >= 0 && blk < a.capacity) slot[i] = blk * bs + pos[i] - page * bs;
+        else bad_block = true;
+      }
     }
-    a.slot_mapping[t] = slot;
-    a.positions[t] = pos;
+    if (wide && t0 + 4 <= a.n_tokens) {
+      *reinterpret_cast<int4*>(a.slot_mapping + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t0 + i >= a.n_tokens) break;
+        a.slot_mapping[t0 + i] = slot[i];
+        a.positions[t0 + i] = pos[i];
+      }
+    }
   }
   if (bad_block) *a.status = ALA_STEP_BAD_BLOCK;
 }
@@ -189,9 +227,10 @@ template <typename V>
 __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a, int lanes) {
   constexpr int U = 4;
   const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+  dependency_wait();
   if (t >= a.n_tokens) return;
   const int lane = threadIdx.x & (lanes - 1);
-  const int64_t slot = __ldg(a.slots + t);
+  const int64_t slot = a.slots[t];
   if (slot < 0 || slot >= a.n_slots) return;
   const int64_t nk = a.key_row / sizeof(V), nv = a.value_row / sizeof(V);
   const V* ks = reinterpret_cast<const V*>(a.key + t * a.key_stride);
@@ -220,30 +259,47 @@ cudaError_t write_as(const PagedWriteArgs& a, cudaStream_t stream) {
   int lanes = 1;
   while (lanes < 256 && lanes * 4 < n) lanes *= 2;
   const int64_t per_block = 256 / lanes;
-  paged_write_kernel<V><<<(unsigned)((a.n_tokens + per_block - 1) / per_block), 256, 0, stream>>>(a, lanes);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.n_tokens + per_block - 1) / per_block));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_write_kernel<V>, a, lanes);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_step(const PagedStepArgs& a, cudaStream_t stream) {
   const int smem = (int)sizeof(StepRow) * (a.batch + 1);
-  cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(StepRow) * (kPagedStepMaxBatch + 1));
-  if (e != cudaSuccess) return e;
+  const bool small = a.n_tokens <= 1024 && a.batch <= 256;
+  if (!small) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  if (smem > 40 * 1024) {  // above what a kernel may have without asking
+    const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(StepRow) * (kPagedStepMaxBatch + 1));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
-  const int ctas = a.n_tokens > 2 * kStepThreads || a.batch > kStepThreads ? kStepCluster : 1;
+  const int ctas = small ? 1 : kStepCluster;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kStepThreads);
+  cfg.blockDim = dim3(small ? 256 : kStepThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, paged_step_kernel, a);
 }
 

@@ -192,7 +192,7 @@ extern "C" int ala_op_bind_workspace(ala_op* op, void* workspace, uint64_t works
   op->mla.bound_ws = nullptr;
   op->paged_attn.bound_ws = nullptr;
   if (paged) {  // no schedule: only the status words have an initial value
-    if (cudaMemsetAsync(workspace, 0, kPagedStatusBytes, st) != cudaSuccess)
+    if (cudaMemsetAsync(workspace, 0, kPagedHeaderBytes, st) != cudaSuccess)
       return fail(ALA_CUDA_ERROR, "%s: status clear failed: %s", fn, cudaGetErrorString(cudaGetLastError()));
   } else if (mla) {
     char err[512] = {0};

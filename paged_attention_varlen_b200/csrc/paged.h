@@ -28,8 +28,9 @@ struct PagedPlan {
   const void* bound_ws = nullptr;  // a workspace whose status words are clear (ala_op_bind_workspace)
 };
 
-// The workspace's first words are the status words; the rest needs no initial values.
-constexpr uint64_t kPagedStatusBytes = 256;
+// The workspace starts with the status words and, from byte 256, a counter for each CTA; both start out as zeros, and
+// an execution leaves the counters so.  The rest needs no initial values.
+constexpr uint64_t kPagedHeaderBytes = 1024;
 
 // Kernel head size (columns of a K / V row: 64, 128 or 256) that serves rows of `row` elements; 0: none.
 int paged_kernel_d(int64_t row);

@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     mbar_init(fin, 1);
     fence_mbar_init();
   }
+  dependency_wait();
   find_start<TK, C::THREADS>(p, &st, red);
   __syncthreads();
   if (st.b < 0) {  // fewer tiles than CTAs
@@ -588,10 +589,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       // partials: slot 1 when the item starts here, 0 when it began in an earlier CTA
       const int64_t prow0 = ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * (NB * 128);
       if (!whole && w.t0 == 0 && threadIdx.x == 0) {
-        // the last CTA c with c * total / ctas <= last tile
-        const int64_t last = line + w.n - 1;
         PagedDesc d;
-        d.n_seg = (int)(((last + 1) * st.ctas - 1) / st.total) - (int)blockIdx.x + 1;
+        d.n_seg = st.part_of(line + w.n - 1) - (int)blockIdx.x + 1;
         d.token0 = (int)token0;
         d.tokens = tokens;
         d.kv_head = w.h;
@@ -820,117 +819,16 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
 
 // ---------------------------------------------------------------------------------------------- combine
 
-template <int N>
-__device__ __forceinline__ void load_f(const float* src, float (&v)[N]) {
-  if constexpr (N == 2) {
-    const float2 a = *reinterpret_cast<const float2*>(src);
-    v[0] = a.x;
-    v[1] = a.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 a = reinterpret_cast<const float4*>(src)[i];
-      v[4 * i] = a.x;
-      v[4 * i + 1] = a.y;
-      v[4 * i + 2] = a.z;
-      v[4 * i + 3] = a.w;
-    }
-  }
-}
-
-// Joins the segments of the items that CTA boundaries cut, one warp per output row (both maps of a
-// differential row), in segment order: m = max_s m_s, O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+// Joins the segments of the items that CTA boundaries cut, one warp per output row.  A grid of its own: the rows of
+// a chunk are too many for the CTAs that cut them to do it on the side.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependency_wait();
   const PagedDesc d = p.desc[blockIdx.x];
   if (d.n_seg == 0) return;
-  constexpr int NB = D == 256 ? 1 : 2;
-  constexpr int N = D / 32;                   // columns per lane
-  constexpr int NW = (kGrid + 31) / 32;       // segment weights per lane
-  const int lane = threadIdx.x & 31;
-  const int maps = p.maps(), gh = p.group / maps;
-  const int col = lane * N;
-  for (int u = blockIdx.y * 8 + (threadIdx.x >> 5); u < d.tokens * gh; u += kCombineY * 8) {
-    float y[N];
-    float lse = 0.f;
-    const int tok = u / gh, token = d.token0 + tok, head = (d.kv_head * gh + u % gh) * maps;
-    for (int map = 0; map < maps; ++map) {
-      const int r = partial_row(p, d.two, tok, u % gh, map);
-      // segment s lies in CTA blockIdx.x + s: in its slot 1 where the item starts, in slot 0 after that
-      auto prow = [&](int s) { return ((int64_t)(blockIdx.x + s) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r; };
-      float wt[NW], top = -INFINITY, sum = 0.f;
-      float2 ml[NW];
-#pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const int s = k * 32 + lane;
-        ml[k] = s < d.n_seg ? p.ml[prow(s)] : make_float2(-INFINITY, 0.f);
-        top = fmaxf(top, ml[k].x);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        wt[k] = fast_exp2(ml[k].x - base);
-        sum = fmaf(ml[k].y, wt[k], sum);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      float acc[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const int n = min(32, d.n_seg - k * 32);
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-          const float f = __shfl_sync(0xffffffffu, wt[k], s);
-          if (col < p.row) {
-            float v[N];
-            load_f<N>(p.part + prow(k * 32 + s) * D + col, v);
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(f, v[i], acc[i]);
-          }
-        }
-      }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      if (map == 0) {
-        lse = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = acc[i] * inv;
-      } else {
-        const float f = -p.lambda[head >> 1] * inv;
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = fmaf(f, acc[i], y[i]);
-      }
-    }
-    if (maps == 2) {
-      float post = p.out_scale;
-      if (p.norm_weight) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);
-    } else if (p.lse && lane == 0) {
-      if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + tok);
-      p.lse[(int64_t)token * p.heads + head] = lse;
-    }
-    if (col < p.row) {
-      uint32_t o[N / 2];
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1], (T*)nullptr);
-      T* dst = static_cast<T*>(p.out) + ((int64_t)token * (p.heads / maps) + head / maps) * p.row + col;
-      if constexpr (N == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
-      else if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
+  const int gh = p.group / p.maps();
+  for (int u = blockIdx.y * 8 + (threadIdx.x >> 5); u < d.tokens * gh; u += kCombineY * 8)
+    combine_row<T, D>(p, d, blockIdx.x, u / gh, u % gh);
 }
 
 template <typename T, int D, int NQ>
@@ -940,30 +838,18 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Pa
   constexpr int kSmem = C::SMEM > 120 * 1024 ? C::SMEM : 120 * 1024;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<T, D, NQ><<<kGrid, C::THREADS, kSmem, stream>>>(tmK, tmV, p);
-  return cudaGetLastError();
+  return launch_dependent(paged_attn_kernel<T, D, NQ>, dim3(kGrid), C::THREADS, kSmem, stream, tmK, tmV, p);
 }
 
 template <typename T, int D>
 cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool few, bool two, cudaStream_t stream) {
+  if (few) return launch_paged_few(std::is_same_v<T, __half> ? kF16 : kBF16, D, tmK, tmV, p, stream);
   cudaError_t e;
-  if (few) e = launch_paged_few(std::is_same_v<T, __half> ? kF16 : kBF16, D, tmK, tmV, p, stream);
-  else if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
+  if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
   else if constexpr (D == 64) e = launch_attn<T, D, 2>(tmK, tmV, p, stream);
   else e = two ? launch_attn<T, D, 2>(tmK, tmV, p, stream) : launch_attn<T, D, 1>(tmK, tmV, p, stream);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent launch: the combine grid is scheduled during the attention kernel's tail, and
-  // griddepcontrol.wait holds it until that kernel has completed
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kGrid, kCombineY);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D>, p);
+  return launch_dependent(paged_combine_kernel<T, D>, dim3(kGrid, kCombineY), 256, 0, stream, p);
 }
 
 uint64_t align256(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -977,7 +863,7 @@ int paged_kernel_d(int64_t row) {
 
 void paged_layout(PagedPlan* plan) {
   const int D = paged_kernel_d(plan->row), rows = D == 256 ? 128 : 256;
-  plan->off_desc = kPagedStatusBytes;
+  plan->off_desc = kPagedHeaderBytes;
   plan->off_ml = align256(plan->off_desc + sizeof(PagedDesc) * kGrid);
   plan->off_part = align256(plan->off_ml + sizeof(float2) * kGrid * 2 * rows);
   plan->ws_size = plan->off_part + (uint64_t)sizeof(float) * kGrid * 2 * rows * D;
@@ -1001,7 +887,7 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaError_t e = cudaSuccess;
-  if (workspace != plan->bound_ws) e = cudaMemsetAsync(workspace, 0, kPagedStatusBytes, stream);
+  if (workspace != plan->bound_ws) e = cudaMemsetAsync(workspace, 0, kPagedHeaderBytes, stream);
   if (e == cudaSuccess) {
     PagedParams p{};
     p.seq_len = plan->seq_len;
@@ -1014,6 +900,7 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     p.out = plan->out;
     p.lse = plan->lse;
     p.status = reinterpret_cast<int*>(ws);
+    p.arrived = reinterpret_cast<int*>(ws + 256);
     p.desc = reinterpret_cast<PagedDesc*>(ws + plan->off_desc);
     p.ml = reinterpret_cast<float2*>(ws + plan->off_ml);
     p.part = reinterpret_cast<float*>(ws + plan->off_part);
@@ -1036,6 +923,11 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     const bool two = D == 64 || (D == 128 && plan->n_tokens * p.group > (int64_t)128 * p.batch);
     p.tb = few ? kFewRows / p.group : !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
     p.box_rows = box;
+    // Few rows: where a kv head's row does not fill the lines that L2 and HBM move, neighbouring heads share them, so
+    // the heads run side by side (CTA c takes head c % kvHeadNum) and find them in L2.  Below 140 busy SMs that would
+    // cost more than it gives.  Measured with 8 kv heads: rows of 160 bytes 690 -> XXX us, of 128 bytes 391 -> XXX us.
+    const int parts = kGrid / p.kv_heads;
+    p.head_stride = few && plan->row * 2 % 256 != 0 && parts * p.kv_heads >= 140 ? p.kv_heads : 1;
     p.scale_log2 = plan->qk_scale * kLog2e;
     p.norm_eps = plan->norm_eps;
     p.out_scale = plan->out_scale;

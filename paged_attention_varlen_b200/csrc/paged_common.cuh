@@ -17,7 +17,7 @@ constexpr int kGrid = 148;                 // one CTA per SM of a B200
 
 // What a split item's first CTA leaves for the combine kernel.
 struct PagedDesc {
-  int32_t n_seg;    // CTAs that hold a segment of the item (0: this CTA starts no split item)
+  int32_t n_seg;    // CTAs that hold a segment of the item (0: this CTA starts no split item); head_stride apart
   int32_t token0;   // first token of the row tile
   int32_t tokens;   // its tokens
   int32_t kv_head;
@@ -32,6 +32,7 @@ struct PagedParams {
   void* out;
   float* lse;
   int* status;
+  int* arrived;     // [kGrid]: segments of the item that starts in a CTA (few rows), 0 between executions
   PagedDesc* desc;  // [kGrid]
   float2* ml;       // [kGrid][2][128 NB]: running max (log2 units) and sum of each partial row
   float* part;      // [kGrid][2][128 NB][D]
@@ -41,6 +42,7 @@ struct PagedParams {
   int32_t tb1, tb;                 // tokens of one block of rows (128 / group), tokens per row tile
   int32_t dq, row;                 // query head size, elements of a K / V row
   int32_t box_rows;
+  int32_t head_stride;             // 1: the line holds all kv heads; kv_heads: a line for each, CTA c on that of head c % kv_heads
   float scale_log2, norm_eps, out_scale;
 
   __host__ __device__ int maps() const { return dq == row ? 1 : 2; }
@@ -183,8 +185,8 @@ struct Walker {
     t0 = 0;
     if (++rt == s.tiles) {
       rt = 0;
-      if (++h == p.kv_heads) {
-        h = 0;
+      if (p.head_stride > 1 || ++h == p.kv_heads) {
+        if (p.head_stride == 1) h = 0;
         do {
           cu += raw;
           if (++b >= p.batch) return false;
@@ -203,8 +205,14 @@ struct Walker {
 struct Start {
   int b, h, rt, t0, raw;
   Seq s;
-  int64_t cu, left, line, total;  // line: this CTA's first tile on the line of `total` tiles
-  int ctas;                       // CTAs that take part
+  int64_t cu, left, line, total;  // line: this CTA's first tile on its line of `total` tiles
+  int parts;                      // CTAs that share the line
+
+  // The part q of a tile: the last with q * total / parts <= tile.
+  __device__ __forceinline__ int part_of(int64_t tile) const {
+    return total < (1 << 24) ? (int)(((unsigned)(tile + 1) * (unsigned)parts - 1) / (unsigned)total)
+                             : (int)(((tile + 1) * parts - 1) / total);
+  }
 };
 
 // Every thread of the CTA scans the batch (kThreads sequences at a time); the results are in *st after the
@@ -242,7 +250,7 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
     cu0 = add(cu0, sum);
     s = make_seq(p, cu, raw, keys);
     per_head = b < p.batch && s.seq > 0 ? tiles_before<TK>(p, s, s.tiles) : 0;
-    w = per_head * p.kv_heads;
+    w = p.head_stride > 1 ? per_head : per_head * p.kv_heads;
     if (blockIdx.x == 0 && b < p.batch && (s.seq != len || s.kv != keys)) atomicCAS(p.status + 1, 0, kDevBadLength);
     int64_t z = w;
 #pragma unroll
@@ -264,17 +272,18 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
   };
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) scan(b0);
   const int64_t total = w0;
-  const int ctas = (int)min((int64_t)gridDim.x, total);
+  const int parts = (int)min((int64_t)(gridDim.x / p.head_stride), total);
+  const int part = blockIdx.x / p.head_stride;
   if (threadIdx.x == 0) {
     st->total = total;
-    st->ctas = ctas;
+    st->parts = parts;
     st->b = -1;
   }
-  if ((int)blockIdx.x >= ctas) return;
+  if (part >= parts) return;
   // 64-bit division only where the numbers need it
   const bool small = total < (1 << 24);
-  const int64_t start = small ? (unsigned)total * blockIdx.x / (unsigned)ctas : blockIdx.x * total / ctas;
-  const int64_t end = small ? (unsigned)total * (blockIdx.x + 1) / (unsigned)ctas : (blockIdx.x + 1) * total / ctas;
+  const int64_t start = small ? (unsigned)total * part / (unsigned)parts : part * total / parts;
+  const int64_t end = small ? (unsigned)total * (part + 1) / (unsigned)parts : (part + 1) * total / parts;
   __syncthreads();
   auto place = [&](int b0) {
     if (w > 0 && w_before <= start && start < w_before + w) {
@@ -284,8 +293,10 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
       st->cu = cu;
       st->line = start;
       st->left = end - start;
-      st->h = small ? (int)((unsigned)(start - w_before) / (unsigned)per_head) : (int)((start - w_before) / per_head);
-      red[0] = start - w_before - st->h * per_head;  // tile within the head
+      int h = 0;
+      if (p.head_stride == 1) h = small ? (int)((unsigned)(start - w_before) / (unsigned)per_head) : (int)((start - w_before) / per_head);
+      red[0] = start - w_before - h * per_head;  // tile within the head
+      st->h = p.head_stride > 1 ? blockIdx.x % p.head_stride : h;
     }
   };
   if (p.batch <= kThreads) {
@@ -316,6 +327,141 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
       st->t0 = (int)(tile - tiles_before<TK>(p, q, lo));
     }
   }
+}
+
+// ---------------------------------------------------------------------------------------------- joining segments
+
+template <int N>
+__device__ __forceinline__ void load_f(const float* src, float (&v)[N]) {
+  if constexpr (N == 2) {
+    const float2 a = __ldcg(reinterpret_cast<const float2*>(src));
+    v[0] = a.x;
+    v[1] = a.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + i);
+      v[4 * i] = a.x;
+      v[4 * i + 1] = a.y;
+      v[4 * i + 2] = a.z;
+      v[4 * i + 3] = a.w;
+    }
+  }
+}
+
+// One output row (token of the tile, head of the group; both maps of a differential row) of an item that starts in
+// CTA `first`, by one warp, its segments in order:
+//   m = max_s m_s, O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+// Other CTAs wrote them, so they are read past L1.
+template <typename T, int D>
+__device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDesc& d, int first, int tok, int hh) {
+  constexpr int NB = D == 256 ? 1 : 2;
+  constexpr int N = D / 32;                   // columns per lane
+  constexpr int NW = (kGrid + 31) / 32;       // segment weights per lane
+  const int lane = threadIdx.x & 31;
+  const int maps = p.maps(), gh = p.group / maps;
+  const int col = lane * N;
+  float y[N];
+  float lse = 0.f;
+  const int token = d.token0 + tok, head = (d.kv_head * gh + hh) * maps;
+  for (int map = 0; map < maps; ++map) {
+    const int r = partial_row(p, d.two, tok, hh, map);
+    // segment s lies in CTA first + s * head_stride: in its slot 1 where the item starts, in slot 0 after that
+    auto prow = [&](int s) { return ((int64_t)(first + s * p.head_stride) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r; };
+    float wt[NW], top = -INFINITY, sum = 0.f;
+    float2 ml[NW];
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int s = k * 32 + lane;
+      ml[k] = s < d.n_seg ? __ldcg(p.ml + prow(s)) : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      wt[k] = fast_exp2(ml[k].x - base);
+      sum = fmaf(ml[k].y, wt[k], sum);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int n = min(32, d.n_seg - k * 32);
+#pragma unroll 8
+      for (int s = 0; s < n; ++s) {
+        const float f = __shfl_sync(0xffffffffu, wt[k], s);
+        if (col < p.row) {
+          float v[N];
+          load_f<N>(p.part + prow(k * 32 + s) * D + col, v);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (map == 0) {
+      lse = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = acc[i] * inv;
+    } else {
+      const float f = -p.lambda[head >> 1] * inv;
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = fmaf(f, acc[i], y[i]);
+    }
+  }
+  if (maps == 2) {
+    float post = p.out_scale;
+    if (p.norm_weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);
+  } else if (p.lse && lane == 0) {
+    if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + tok);
+    p.lse[(int64_t)token * p.heads + head] = lse;
+  }
+  if (col < p.row) {
+    uint32_t o[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1], (T*)nullptr);
+    T* dst = static_cast<T*>(p.out) + ((int64_t)token * (p.heads / maps) + head / maps) * p.row + col;
+    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
+    else if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- launches
+
+// Every kernel here is a programmatic dependent launch: it is scheduled while the one before it on the stream ends,
+// and waits here, before it touches memory, until that has completed.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next such kernel be scheduled from now on (it waits all the same).
+__device__ __forceinline__ void dependency_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Rows of at most kFewRows queries per kv head (paged_few.cu).

@@ -49,6 +49,8 @@ struct RowTables {
   int last_key[kFewRows];      // keys up to this one are allowed (-1: none)
   float m[kFewRows];
   float red[4][kFewRows];      // per lane quarter
+  PagedDesc join;              // n_seg != 0: this CTA's segment was the last of a cut item to arrive
+  int first;                   // the CTA where that starts
 };
 
 __device__ __forceinline__ bool any_of_256(bool x) {
@@ -402,13 +404,14 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
+  dependency_wait();
+  dependency_trigger();
   find_start<128, C::THREADS>(p, &st, red);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (st.b < 0) {  // fewer tiles than CTAs
-    if (threadIdx.x == 0) p.desc[blockIdx.x].n_seg = 0;
     if (warp == kWarpMma) tmem_dealloc(tmem, C::TMEM_COLS);
     return;
   }
@@ -557,7 +560,6 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     const int group = p.group, maps = p.maps();
     FewState f{0, 0, true};
     uint32_t loads = 0;  // ring slots used so far
-    bool owner = false;
     int64_t line = st.line;
     do {
       const int tokens = w.tokens(p), rows = tokens * group, cnt = w.t1 - w.t0;
@@ -590,19 +592,6 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       const uint32_t v0 = loads + (cnt > 1 ? 2 : 1);  // the first tile's V in the order of loads
       uint64_t* v_full0 = full + v0 % NS;
       const uint32_t v_phase0 = (v0 / NS) & 1;
-      if (w.t0 == 0 && w.t1 < w.n && r == 0) {
-        // a cut item starts here; the last CTA c with c * total / ctas <= last tile
-        const int64_t last = line + w.n - 1;
-        PagedDesc d;
-        d.n_seg = (int)(((last + 1) * st.ctas - 1) / st.total) - (int)blockIdx.x + 1;
-        d.token0 = (int)token0;
-        d.tokens = tokens;
-        d.kv_head = w.h;
-        d.pos0 = w.rt * p.tb + off;
-        d.two = 0;
-        p.desc[blockIdx.x] = d;
-        owner = true;
-      }
       const uint32_t sp = smem_addr(sP);
       if (R == 8)
         few_item<T, D, 8>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
@@ -611,9 +600,29 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       else
         few_item<T, D, 32>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
       loads += 2 * cnt;
+      if (w.t0 > 0 || w.t1 < w.n) {
+        // ---- a cut item: whoever brings its last segment joins them, so nobody waits
+        __threadfence();
+        named_barrier_sync(1, 256);
+        if (r == 0) {
+          const int64_t tile0 = line - w.t0;
+          const int q0 = st.part_of(tile0), n_seg = st.part_of(tile0 + w.n - 1) - q0 + 1;
+          const int first = q0 * p.head_stride + (p.head_stride > 1 ? w.h : 0);
+          const bool last = f.ok && atomicAdd(p.arrived + first, 1) == n_seg - 1;
+          if (last) p.arrived[first] = 0;  // for the next execution
+          __threadfence();
+          tab.join = PagedDesc{last ? n_seg : 0, (int)token0, tokens, w.h, w.rt * p.tb + off, 0};
+          tab.first = first;
+        }
+        named_barrier_sync(1, 256);
+        const PagedDesc d = tab.join;
+        if (d.n_seg != 0) {
+          const int gh = group / maps;
+          for (int o = warp; o < tokens * gh; o += 8) combine_row<T, D>(p, d, tab.first, o / gh, o % gh);
+        }
+      }
       line += cnt;
     } while (w.next(p));
-    if (r == 0 && !owner) p.desc[blockIdx.x].n_seg = 0;
   }
 
   __syncwarp();
@@ -630,8 +639,7 @@ cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedPa
   using C = Few<T, D>;
   const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  paged_few_kernel<T, D><<<kGrid, C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
-  return cudaGetLastError();
+  return launch_dependent(paged_few_kernel<T, D>, dim3(kGrid), C::THREADS, C::SMEM, stream, tmK, tmV, p);
 }
 
 }  // namespace

@@ -262,16 +262,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
 
   Walker<TK> w;
-  w.b = st.b;
-  w.h = st.h;
-  w.rt = st.rt;
-  w.t0 = st.t0;
-  w.raw = st.raw;
-  w.cu = st.cu;
-  w.left = st.left;
-  w.s = st.s;
-  w.fetch(p);
-  w.enter(p);
+  w.begin(p, st);
 
   // An item of cnt tiles is U steps: step u fills S buffer u & 1 and multiplies its P.  With two blocks of rows,
   // steps 2i and 2i + 1 are tile i for block 0 and 1; otherwise step u is tile u, for block u & 1 of the two that

@@ -103,7 +103,7 @@ struct Seq {
   int seq, kv, tiles;  // new tokens, keys, row tiles
 };
 
-__device__ __forceinline__ int raw_len(const PagedParams& p, int b) { return min(max(__ldg(p.seq_len + b), 0), p.n_tokens); }
+__device__ __forceinline__ int clamp_len(const PagedParams& p, int len) { return min(max(len, 0), p.n_tokens); }
 
 __device__ __forceinline__ Seq make_seq(const PagedParams& p, int64_t cu, int raw, int kv) {
   Seq s;
@@ -161,19 +161,44 @@ __device__ int64_t tiles_before(const PagedParams& p, const Seq& s, int r) {
   return last + ones + (m > 0 ? floor_sum((uint32_t)m, TK, p.tb, (uint64_t)(off + (int64_t)(ones + 1) * p.tb + TK - 1)) : 0);
 }
 
+struct Start {
+  int b, h, rt, t0, raw;
+  Seq s;
+  int64_t cu, left, line, total;  // line: this CTA's first tile on its line of `total` tiles
+  int parts;                      // CTAs that share the line
+
+  // The part q of a tile: the last with q * total / parts <= tile.
+  __device__ __forceinline__ int part_of(int64_t tile) const {
+    return total < (1 << 24) ? (int)(((unsigned)(tile + 1) * (unsigned)parts - 1) / (unsigned)total)
+                             : (int)(((tile + 1) * parts - 1) / total);
+  }
+};
+
 // A CTA's position on the work line: item (b, h, rt) and its tiles [t0, t1) of n.
 template <int TK>
 struct Walker {
   int b, h, rt, t0, t1, n;
-  int raw, raw_next, kv_next;  // the next sequence's lengths are fetched ahead, so that no item waits for them
+  int raw, len_next, kv_next;  // the next sequence's lengths, as they lie in memory, are fetched ahead of their use
   int64_t cu, left;
   Seq s;
 
   __device__ __forceinline__ void fetch(const PagedParams& p) {
     if (b + 1 < p.batch) {
-      raw_next = raw_len(p, b + 1);
+      len_next = __ldg(p.seq_len + b + 1);
       kv_next = __ldg(p.kv_seq_len + b + 1);
     }
+  }
+  __device__ __forceinline__ void begin(const PagedParams& p, const Start& st) {
+    b = st.b;
+    h = st.h;
+    rt = st.rt;
+    t0 = st.t0;
+    raw = st.raw;
+    cu = st.cu;
+    left = st.left;
+    s = st.s;
+    fetch(p);
+    enter(p);
   }
   __device__ __forceinline__ void enter(const PagedParams& p) {
     n = key_tiles<TK>(p, s, rt);
@@ -190,7 +215,7 @@ struct Walker {
         do {
           cu += raw;
           if (++b >= p.batch) return false;
-          raw = raw_next;
+          raw = clamp_len(p, len_next);
           s = make_seq(p, cu, raw, kv_next);
           fetch(p);
         } while (s.seq == 0);
@@ -202,18 +227,109 @@ struct Walker {
   __device__ __forceinline__ int tokens(const PagedParams& p) const { return min(p.tb, s.seq - rt * p.tb); }
 };
 
-struct Start {
-  int b, h, rt, t0, raw;
-  Seq s;
-  int64_t cu, left, line, total;  // line: this CTA's first tile on its line of `total` tiles
-  int parts;                      // CTAs that share the line
+// CTAs that share a line of `total` tiles: no more than give every one as many tiles as the busiest has anyway, so
+// that a short line is not cut for nothing.
+__device__ __forceinline__ int parts_of(const PagedParams& p, int64_t total) {
+  const int most = gridDim.x / p.head_stride;
+  if (total >= 64 * (int64_t)most) return most;
+  const unsigned t = (unsigned)total;
+  if (t == 0) return 0;
+  const unsigned each = (t + most - 1) / most;
+  return (int)((t + each - 1) / each);
+}
 
-  // The part q of a tile: the last with q * total / parts <= tile.
-  __device__ __forceinline__ int part_of(int64_t tile) const {
-    return total < (1 << 24) ? (int)(((unsigned)(tile + 1) * (unsigned)parts - 1) / (unsigned)total)
-                             : (int)(((tile + 1) * parts - 1) / total);
+// First tile of part q; 64-bit division only where the numbers need it.
+__device__ __forceinline__ int64_t cut(int64_t total, int parts, int q) {
+  return total < (1 << 24) ? (unsigned)total * (unsigned)q / (unsigned)parts : q * total / parts;
+}
+
+// The row tile that holds a tile of the head, by a whole warp, 32 candidates a round.
+template <int TK>
+__device__ __forceinline__ int find_row_tile(const PagedParams& p, const Seq& q, int64_t tile) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = q.tiles;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int c = lo + (lane + 1) * step;
+    const bool below = c < hi && tiles_before<TK>(p, q, c) <= tile;
+    const int k = __popc(__ballot_sync(0xffffffffu, below));
+    lo += k * step;
+    hi = min(hi, lo + step);
   }
-};
+  return lo;
+}
+
+// The same as find_start for a batch of at most 64 sequences, by every warp for itself: two sequences a lane, all in
+// registers, no meeting of the warps.  A single token of a single user spends 2 us less here.
+template <int TK>
+__device__ __forceinline__ void find_start_small(const PagedParams& p, Start& st) {
+  const int lane = threadIdx.x & 31;
+  int len[2], keys[2], raw[2], cu[2];
+  int64_t w[2], before[2], per_head[2];
+  Seq s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = 2 * lane + k;
+    len[k] = b < p.batch ? __ldg(p.seq_len + b) : 0;
+    keys[k] = b < p.batch ? __ldg(p.kv_seq_len + b) : 0;
+  }
+  raw[0] = clamp_len(p, len[0]);
+  raw[1] = clamp_len(p, len[1]);
+  int64_t x = (int64_t)raw[0] + raw[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  x -= (int64_t)raw[0] + raw[1];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t at = x + (k ? raw[0] : 0);
+    cu[k] = (int)min(at, (int64_t)0x7fffffff);
+    s[k] = make_seq(p, at, raw[k], keys[k]);
+    per_head[k] = s[k].seq > 0 ? tiles_before<TK>(p, s[k], s[k].tiles) : 0;
+    w[k] = p.head_stride > 1 ? per_head[k] : per_head[k] * p.kv_heads;
+    if (blockIdx.x == 0 && threadIdx.x < 32 && 2 * lane + k < p.batch && (s[k].seq != len[k] || s[k].kv != keys[k]))
+      atomicCAS(p.status + 1, 0, kDevBadLength);
+  }
+  int64_t z = w[0] + w[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, z, o);
+    if (lane >= o) z += y;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, z, 31);
+  before[0] = z - w[0] - w[1];
+  before[1] = z - w[1];
+  const int parts = parts_of(p, total), part = blockIdx.x / p.head_stride;
+  st.total = total;
+  st.parts = parts;
+  st.b = -1;
+  if (part >= parts) return;
+  const int64_t start = cut(total, parts, part), end = cut(total, parts, part + 1);
+  const bool in1 = before[1] <= start && start < before[1] + w[1];
+  const bool in0 = before[0] <= start && start < before[0] + w[0];
+  const int src = __ffs(__ballot_sync(0xffffffffu, in0 || in1)) - 1;
+  const int k = __shfl_sync(0xffffffffu, (int)in1, src);
+  auto pick = [&](auto a0, auto a1) { return __shfl_sync(0xffffffffu, k ? a1 : a0, src); };
+  st.b = 2 * src + k;
+  st.raw = pick(raw[0], raw[1]);
+  st.cu = pick(cu[0], cu[1]);
+  st.s.seq = pick(s[0].seq, s[1].seq);
+  st.s.kv = pick(s[0].kv, s[1].kv);
+  st.s.tiles = pick(s[0].tiles, s[1].tiles);
+  int64_t tile = start - pick(before[0], before[1]);
+  const int64_t each = pick(per_head[0], per_head[1]);
+  st.line = start;
+  st.left = end - start;
+  st.h = blockIdx.x % p.head_stride;
+  if (p.head_stride == 1) {
+    st.h = total < (1 << 24) ? (int)((unsigned)tile / (unsigned)each) : (int)(tile / each);
+    tile -= st.h * each;
+  }
+  st.rt = find_row_tile<TK>(p, st.s, tile);
+  st.t0 = (int)(tile - tiles_before<TK>(p, st.s, st.rt));
+}
 
 // Every thread of the CTA scans the batch (kThreads sequences at a time); the results are in *st after the
 // caller's __syncthreads.  `red` holds 2 * kThreads / 32 words.
@@ -231,7 +347,7 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
   auto scan = [&](int b0) {
     const int b = b0 + threadIdx.x;
     const int len = b < p.batch ? __ldg(p.seq_len + b) : 0, keys = b < p.batch ? __ldg(p.kv_seq_len + b) : 0;
-    raw = min(max(len, 0), p.n_tokens);
+    raw = clamp_len(p, len);
     int x = raw;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -272,7 +388,7 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
   };
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) scan(b0);
   const int64_t total = w0;
-  const int parts = (int)min((int64_t)(gridDim.x / p.head_stride), total);
+  const int parts = parts_of(p, total);
   const int part = blockIdx.x / p.head_stride;
   if (threadIdx.x == 0) {
     st->total = total;
@@ -280,10 +396,8 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
     st->b = -1;
   }
   if (part >= parts) return;
-  // 64-bit division only where the numbers need it
   const bool small = total < (1 << 24);
-  const int64_t start = small ? (unsigned)total * part / (unsigned)parts : part * total / parts;
-  const int64_t end = small ? (unsigned)total * (part + 1) / (unsigned)parts : (part + 1) * total / parts;
+  const int64_t start = cut(total, parts, part), end = cut(total, parts, part + 1);
   __syncthreads();
   auto place = [&](int b0) {
     if (w > 0 && w_before <= start && start < w_before + w) {
@@ -313,15 +427,7 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
   if (warp == 0) {
     const Seq q = st->s;
     const int64_t tile = red[0];
-    int lo = 0, hi = q.tiles;  // the row tile lies in [lo, hi): 32 candidates a round
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int c = lo + (lane + 1) * step;
-      const bool below = c < hi && tiles_before<TK>(p, q, c) <= tile;
-      const int k = __popc(__ballot_sync(0xffffffffu, below));
-      lo += k * step;
-      hi = min(hi, lo + step);
-    }
+    const int lo = find_row_tile<TK>(p, q, tile);
     if (lane == 0) {
       st->rt = lo;
       st->t0 = (int)(tile - tiles_before<TK>(p, q, lo));
@@ -352,74 +458,87 @@ __device__ __forceinline__ void load_f(const float* src, float (&v)[N]) {
 // One output row (token of the tile, head of the group; both maps of a differential row) of an item that starts in
 // CTA `first`, by one warp, its segments in order:
 //   m = max_s m_s, O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
-// Other CTAs wrote them, so they are read past L1.
+// Other CTAs wrote them, so they are read past L1.  Latency is all it costs: the statistics and the first U segments'
+// values are fetched together, and the maps too.
 template <typename T, int D>
 __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDesc& d, int first, int tok, int hh) {
   constexpr int NB = D == 256 ? 1 : 2;
   constexpr int N = D / 32;                   // columns per lane
   constexpr int NW = (kGrid + 31) / 32;       // segment weights per lane
+  constexpr int U = D == 256 ? 4 : 8;         // segments in flight
   const int lane = threadIdx.x & 31;
   const int maps = p.maps(), gh = p.group / maps;
   const int col = lane * N;
-  float y[N];
-  float lse = 0.f;
   const int token = d.token0 + tok, head = (d.kv_head * gh + hh) * maps;
-  for (int map = 0; map < maps; ++map) {
-    const int r = partial_row(p, d.two, tok, hh, map);
-    // segment s lies in CTA first + s * head_stride: in its slot 1 where the item starts, in slot 0 after that
-    auto prow = [&](int s) { return ((int64_t)(first + s * p.head_stride) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r; };
-    float wt[NW], top = -INFINITY, sum = 0.f;
-    float2 ml[NW];
+  // segment s lies in CTA first + s * head_stride: in its slot 1 where the item starts, in slot 0 after that
+  int r[2] = {partial_row(p, d.two, tok, hh, 0), maps == 2 ? partial_row(p, d.two, tok, hh, 1) : 0};
+  auto prow = [&](int map, int s) { return ((int64_t)(first + s * p.head_stride) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r[map]; };
+  float2 ml[2][NW];
+#pragma unroll
+  for (int map = 0; map < 2; ++map)
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
       const int s = k * 32 + lane;
-      ml[k] = s < d.n_seg ? __ldcg(p.ml + prow(s)) : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, ml[k].x);
+      ml[map][k] = make_float2(-INFINITY, 0.f);
+      if (map < maps && s < d.n_seg) ml[map][k] = __ldcg(p.ml + prow(map, s));
     }
+  float v[2][U][N];
+  auto fetch = [&](int s0) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
+    for (int map = 0; map < 2; ++map)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (map < maps && s0 + u < d.n_seg && col < p.row) load_f<N>(p.part + prow(map, s0 + u) * D + col, v[map][u]);
+  };
+  fetch(0);
+  float wt[2][NW], top[2], sum[2], acc[2][N];
+#pragma unroll
+  for (int map = 0; map < 2; ++map) {
+    top[map] = -INFINITY;
+    sum[map] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) top[map] = fmaxf(top[map], ml[map][k].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top[map] = fmaxf(top[map], __shfl_xor_sync(0xffffffffu, top[map], o));
+    const float base = top[map] == -INFINITY ? 0.f : top[map];
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      wt[k] = fast_exp2(ml[k].x - base);
-      sum = fmaf(ml[k].y, wt[k], sum);
+      wt[map][k] = fast_exp2(ml[map][k].x - base);
+      sum[map] = fmaf(ml[map][k].y, wt[map][k], sum[map]);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float acc[N];
+    for (int o = 16; o; o >>= 1) sum[map] += __shfl_xor_sync(0xffffffffu, sum[map], o);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      const int n = min(32, d.n_seg - k * 32);
-#pragma unroll 8
-      for (int s = 0; s < n; ++s) {
-        const float f = __shfl_sync(0xffffffffu, wt[k], s);
-        if (col < p.row) {
-          float v[N];
-          load_f<N>(p.part + prow(k * 32 + s) * D + col, v);
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] = fmaf(f, v[i], acc[i]);
-        }
-      }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (map == 0) {
-      lse = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = acc[i] * inv;
-    } else {
-      const float f = -p.lambda[head >> 1] * inv;
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = fmaf(f, acc[i], y[i]);
-    }
+    for (int i = 0; i < N; ++i) acc[map][i] = 0.f;
   }
-  if (maps == 2) {
-    float post = p.out_scale;
-    if (p.norm_weight) {
-      float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) ss = fmaf(y[i], y[i], ss);
+  for (int k = 0; k < NW; ++k)
+    for (int s0 = k * 32; s0 < min(d.n_seg, k * 32 + 32); s0 += U) {
+      if (s0 > 0) fetch(s0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int map = 0; map < 2; ++map) {
+          const float f = __shfl_sync(0xffffffffu, wt[map][k], (s0 + u) & 31);
+          if (map < maps && s0 + u < d.n_seg && col < p.row) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[map][i] = fmaf(f, v[map][u][i], acc[map][i]);
+          }
+        }
+    }
+  float y[N];
+  const float inv = sum[0] > 0.f ? 1.f / sum[0] : 0.f;  // a row without keys gets 0
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = acc[0][i] * inv;
+  if (maps == 2) {
+    const float f = sum[1] > 0.f ? -p.lambda[head >> 1] / sum[1] : 0.f;
+    float post = p.out_scale, ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      y[i] = fmaf(f, acc[1][i], y[i]);
+      ss = fmaf(y[i], y[i], ss);
+    }
+    if (p.norm_weight) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
@@ -427,6 +546,7 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);
   } else if (p.lse && lane == 0) {
+    float lse = sum[0] > 0.f ? top[0] * kLn2 + logf(sum[0]) : -INFINITY;
     if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + tok);
     p.lse[(int64_t)token * p.heads + head] = lse;
   }

@@ -36,7 +36,7 @@ struct Few {
   static constexpr int Q_BYTES = CB * QCB;
   static constexpr int P_BYTES = 2 * QCB;           // [2 blocks of 64 keys][32 rows][128 B]
   static constexpr int N_BARS = 1 + 2 * NS + 6 + 2;
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 352;
   static constexpr int SMEM = 1024 + NS * KV_BYTES + Q_BYTES + 2 * P_BYTES + N_BARS * 8 + 16;
   static constexpr uint32_t O_COL = 64, TMEM_COLS = 128;  // S^T [0, 32) and [32, 64), O^T from 64
   static_assert(SMEM + 1400 <= 232448, "shared memory budget (1400: the static part)");
@@ -49,8 +49,10 @@ struct RowTables {
   int last_key[kFewRows];      // keys up to this one are allowed (-1: none)
   float m[kFewRows];
   float red[4][kFewRows];      // per lane quarter
-  PagedDesc join;              // n_seg != 0: this CTA's segment was the last of a cut item to arrive
-  int first;                   // the CTA where that starts
+  Start start;                 // where this CTA starts, and the scratch of finding it
+  int64_t scan[2 * 12];
+  PagedDesc join[2];           // n_seg != 0: this CTA's segment was the last of a cut item to arrive (a CTA has two at most)
+  int first[2];                // the CTA where that starts
 };
 
 __device__ __forceinline__ bool any_of_256(bool x) {
@@ -358,7 +360,8 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
 
 template <typename T, int D>
 __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
-    paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+    paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PagedParams p) {
   using C = Few<T, D>;
   constexpr int NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
@@ -376,14 +379,12 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   uint64_t* o_done = pv_done + 2;
   uint64_t* fin = o_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
-  __shared__ Start st;
-  __shared__ int64_t red[2 * C::THREADS / 32];
   __shared__ RowTables tab;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   int* status = p.status;
-  constexpr int kWarpLoad = 8, kWarpMma = 9;
+  constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 256);
@@ -406,9 +407,16 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   }
   dependency_wait();
   dependency_trigger();
-  find_start<128, C::THREADS>(p, &st, red);
   tc_fence_before();
-  __syncthreads();
+  Start st;
+  if (p.batch <= 64) {
+    find_start_small<128>(p, st);
+    __syncthreads();
+  } else {
+    find_start<128, C::THREADS>(p, &tab.start, tab.scan);
+    __syncthreads();
+    st = tab.start;
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (st.b < 0) {  // fewer tiles than CTAs
@@ -416,54 +424,32 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     return;
   }
   Walker<128> w;
-  w.b = st.b;
-  w.h = st.h;
-  w.rt = st.rt;
-  w.t0 = st.t0;
-  w.raw = st.raw;
-  w.cu = st.cu;
-  w.left = st.left;
-  w.s = st.s;
-  w.fetch(p);
-  w.enter(p);
+  w.begin(p, st);
 
   // Barrier phases run on across items: the ring by a slot and its phase, the S and P buffers by a counter of tiles
   // (buffer g & 1, phase g / 2), q_full and o_done by items.
-  if (warp == kWarpLoad) {
-    // -------------------------------------------------------------- producer: lane i loads box i of each tile
+  if (warp == kWarpK || warp == kWarpV) {
+    // -------------------------------------------------------------- producers: lane i loads box i of each tile
+    // Two warps, since the boxes of small pages are many and a warp issues one in about 80 cycles; the order of the
+    // ring says which slots are whose.
+    const bool is_k = warp == kWarpK;
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
     const bool leader = elect_one();
-    if (leader) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
+    if (leader) tma_prefetch_desc(map);
     const int bs = p.block_size, box = p.box_rows;
     const bool has_box = lane * box < 128;
     const int oob_row = p.num_blocks * bs;
     bool ok = true;
-    uint32_t g = 0;  // loads so far
-    auto load = [&](const CUtensorMap* map, int row) {
-      const int slot = g % NS;
-      if (ok && g >= (uint32_t)NS)
-        ok = __all_sync(0xffffffffu, mbar_wait(empty + slot, ((g / NS) - 1) & 1, status, kDevTimeoutKEmpty));
-      if (!ok) return;
-      if (leader) mbar_expect_tx(full + slot, C::KV_BYTES);
-      __syncwarp();
-      if (has_box) {
-        uint8_t* dst = ring + slot * C::KV_BYTES + lane * box * 128;
-#pragma unroll
-        for (int cb = 0; cb < C::CB; ++cb) tma_load_3d(dst + cb * (128 * 128), map, full + slot, cb * 64, w.h, row);
-      }
-      __syncwarp();
-      ++g;
-    };
+    uint32_t loads = 0, last = 0;  // ring loads of the items before; this warp's last load
     do {
       const int32_t* bt = p.block_tables + (size_t)w.b * p.max_blocks;
       const int pages = (w.s.kv + bs - 1) / bs;
+      const int cnt = w.t1 - w.t0;
       // the table entry of a tile's box is fetched one tile ahead, so its latency is not in the loop
       int pg = ((w.t1 - 1) * 128 + lane * box) / bs;
       int blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
-      int row_v = 0;
-      for (int j = w.t1 - 1; j >= w.t0; --j) {
+      for (int i = 0; i < cnt && ok; ++i) {
+        const int j = w.t1 - 1 - i;
         const int pos = j * 128 + lane * box;
         int row = oob_row;  // past the last page: the load fills zeros
         if (has_box && pg < pages) {
@@ -474,14 +460,28 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
           pg = (pos - 128) / bs;
           blk = has_box && pg < pages ? __ldg(bt + pg) : -1;
         }
-        load(&tmK, row);
-        if (j < w.t1 - 1) load(&tmV, row_v);
-        row_v = row;
+        // K(0), K(1), V(0), K(2), V(1), ..., V(cnt - 1)
+        const uint32_t g = loads + (is_k ? (i == 0 ? 0 : 2 * i - 1) : (i == cnt - 1 ? 2 * i + 1 : 2 * i + 2));
+        const uint32_t slot = g % NS;
+        if (g >= (uint32_t)NS)
+          ok = __all_sync(0xffffffffu, mbar_wait(empty + slot, ((g / NS) - 1) & 1, status, kDevTimeoutKEmpty));
+        if (!ok) break;
+        if (leader) mbar_expect_tx(full + slot, C::KV_BYTES);
+        __syncwarp();
+        if (has_box) {
+          uint8_t* dst = ring + slot * C::KV_BYTES + lane * box * 128;
+#pragma unroll
+          for (int cb = 0; cb < C::CB; ++cb) tma_load_3d(dst + cb * (128 * 128), map, full + slot, cb * 64, w.h, row);
+        }
+        __syncwarp();
+        last = g;
       }
-      load(&tmV, row_v);
+      loads += 2 * cnt;
     } while (ok && w.next(p));
-    // never leave the CTA while loads this warp issued are still landing in shared memory
-    for (uint32_t i = g >= (uint32_t)NS ? g - NS : 0; i < g; ++i) mbar_wait(full + (i % NS), (i / NS) & 1, status, kDevTimeoutKFull);
+    // Never leave the CTA while loads are still landing in shared memory.  The CTA ends when the last tile has been
+    // multiplied, so that can only be after a failure, when these waits return within milliseconds.
+    if (!ok)
+      for (int s = 0; s < NS; ++s) mbar_wait(full + s, (last / NS) & 1, status, is_k ? kDevTimeoutKFull : kDevTimeoutVFull);
     __syncwarp();
   } else if (warp == kWarpMma) {
     // -------------------------------------------------------------- MMA issuer: warp-uniform, one lane issues
@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     const int group = p.group, maps = p.maps();
     FewState f{0, 0, true};
     uint32_t loads = 0;  // ring slots used so far
+    if (r == 0) tab.join[0].n_seg = tab.join[1].n_seg = 0;
     int64_t line = st.line;
     do {
       const int tokens = w.tokens(p), rows = tokens * group, cnt = w.t1 - w.t0;
@@ -602,27 +603,30 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       loads += 2 * cnt;
       if (w.t0 > 0 || w.t1 < w.n) {
         // ---- a cut item: whoever brings its last segment joins them, so nobody waits
-        __threadfence();
         named_barrier_sync(1, 256);
         if (r == 0) {
+          __threadfence();  // with the barrier: all threads' partials come before the count
           const int64_t tile0 = line - w.t0;
           const int q0 = st.part_of(tile0), n_seg = st.part_of(tile0 + w.n - 1) - q0 + 1;
           const int first = q0 * p.head_stride + (p.head_stride > 1 ? w.h : 0);
           const bool last = f.ok && atomicAdd(p.arrived + first, 1) == n_seg - 1;
           if (last) p.arrived[first] = 0;  // for the next execution
-          __threadfence();
-          tab.join = PagedDesc{last ? n_seg : 0, (int)token0, tokens, w.h, w.rt * p.tb + off, 0};
-          tab.first = first;
-        }
-        named_barrier_sync(1, 256);
-        const PagedDesc d = tab.join;
-        if (d.n_seg != 0) {
-          const int gh = group / maps;
-          for (int o = warp; o < tokens * gh; o += 8) combine_row<T, D>(p, d, tab.first, o / gh, o % gh);
+          const int k = w.t0 > 0 ? 0 : 1;
+          tab.join[k] = PagedDesc{last ? n_seg : 0, (int)token0, tokens, w.h, w.rt * p.tb + off, 0};
+          tab.first[k] = first;
         }
       }
       line += cnt;
     } while (w.next(p));
+    // ---- the joins that fell to this CTA, both items' rows side by side (after the loop, so that what a join holds in
+    // registers does not weigh on the tiles)
+    if (r == 0) __threadfence();
+    named_barrier_sync(1, 256);
+    const int n0 = tab.join[0].n_seg ? tab.join[0].tokens * group / maps : 0, n1 = tab.join[1].n_seg ? tab.join[1].tokens * group / maps : 0;
+    for (int o = warp; o < n0 + n1; o += 8) {
+      const int k = o < n0 ? 0 : 1, row = o - k * n0, gh = group / maps;
+      combine_row<T, D>(p, tab.join[k], tab.first[k], row / gh, row % gh);
+    }
   }
 
   __syncwarp();

@@ -919,6 +919,11 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     // cost more than it gives.  Measured with 8 kv heads: rows of 160 bytes 690 -> XXX us, of 128 bytes 391 -> XXX us.
     const int parts = kGrid / p.kv_heads;
     p.head_stride = few && plan->row * 2 % 256 != 0 && parts * p.kv_heads >= 140 ? p.kv_heads : 1;
+    {
+      const int tk = few || D != 256 ? 128 : 64;
+      const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
+      p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
+    }
     p.scale_log2 = plan->qk_scale * kLog2e;
     p.norm_eps = plan->norm_eps;
     p.out_scale = plan->out_scale;

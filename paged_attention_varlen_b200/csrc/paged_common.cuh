@@ -42,6 +42,7 @@ struct PagedParams {
   int32_t tb1, tb;                 // tokens of one block of rows (128 / group), tokens per row tile
   int32_t dq, row;                 // query head size, elements of a K / V row
   int32_t box_rows;
+  int32_t small;                   // at most 64 sequences whose lengths, whatever they are, make fewer than 2^24 tiles
   int32_t head_stride;             // 1: the line holds all kv heads; kv_heads: a line for each, CTA c on that of head c % kv_heads
   float scale_log2, norm_eps, out_scale;
 
@@ -109,7 +110,7 @@ __device__ __forceinline__ Seq make_seq(const PagedParams& p, int64_t cu, int ra
   Seq s;
   s.seq = (int)max((int64_t)0, min((int64_t)raw, p.n_tokens - cu));
   s.kv = min(max(kv, 0), p.max_blocks * p.block_size);
-  s.tiles = (int)((unsigned)(s.seq + p.tb - 1) / (unsigned)p.tb);
+  s.tiles = s.seq <= p.tb ? s.seq > 0 : (int)((unsigned)(s.seq + p.tb - 1) / (unsigned)p.tb);
   return s;
 }
 
@@ -152,7 +153,7 @@ __device__ int64_t tiles_before(const PagedParams& p, const Seq& s, int r) {
   int64_t last = 0;
   if (r == s.tiles) {  // the last row tile may be short
     last = key_tiles<TK>(p, s, r - 1);
-    --r;
+    if (--r == 0) return last;
   }
   // full row tile i (from 1) sees off + i tb keys: one tile while that is at most TK, then ceil(. / TK)
   const int off = s.kv - s.seq;
@@ -259,76 +260,76 @@ __device__ __forceinline__ int find_row_tile(const PagedParams& p, const Seq& q,
   return lo;
 }
 
-// The same as find_start for a batch of at most 64 sequences, by every warp for itself: two sequences a lane, all in
-// registers, no meeting of the warps.  A single token of a single user spends 2 us less here.
+// The same as find_start where p.small, by every warp for itself: two sequences a lane, 32-bit numbers in registers,
+// no meeting of the warps.  A single token of a single user spends 2 us less here.
 template <int TK>
 __device__ __forceinline__ void find_start_small(const PagedParams& p, Start& st) {
   const int lane = threadIdx.x & 31;
-  int len[2], keys[2], raw[2], cu[2];
-  int64_t w[2], before[2], per_head[2];
+  int len[2], keys[2], raw[2], w[2], per_head[2];
   Seq s[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int b = 2 * lane + k;
     len[k] = b < p.batch ? __ldg(p.seq_len + b) : 0;
     keys[k] = b < p.batch ? __ldg(p.kv_seq_len + b) : 0;
+    raw[k] = clamp_len(p, len[k]);
   }
-  raw[0] = clamp_len(p, len[0]);
-  raw[1] = clamp_len(p, len[1]);
-  int64_t x = (int64_t)raw[0] + raw[1];
+  int x = raw[0] + raw[1];  // below 64 * 2^24
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  x -= (int64_t)raw[0] + raw[1];
+  const int cu[2] = {x - raw[0] - raw[1], x - raw[1]};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int64_t at = x + (k ? raw[0] : 0);
-    cu[k] = (int)min(at, (int64_t)0x7fffffff);
-    s[k] = make_seq(p, at, raw[k], keys[k]);
-    per_head[k] = s[k].seq > 0 ? tiles_before<TK>(p, s[k], s[k].tiles) : 0;
+    s[k] = make_seq(p, cu[k], raw[k], keys[k]);
+    per_head[k] = s[k].seq > 0 ? (int)tiles_before<TK>(p, s[k], s[k].tiles) : 0;
     w[k] = p.head_stride > 1 ? per_head[k] : per_head[k] * p.kv_heads;
     if (blockIdx.x == 0 && threadIdx.x < 32 && 2 * lane + k < p.batch && (s[k].seq != len[k] || s[k].kv != keys[k]))
       atomicCAS(p.status + 1, 0, kDevBadLength);
   }
-  int64_t z = w[0] + w[1];
+  int z = w[0] + w[1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, z, o);
+    const int y = __shfl_up_sync(0xffffffffu, z, o);
     if (lane >= o) z += y;
   }
-  const int64_t total = __shfl_sync(0xffffffffu, z, 31);
-  before[0] = z - w[0] - w[1];
-  before[1] = z - w[1];
+  const int total = __shfl_sync(0xffffffffu, z, 31);
+  const int before[2] = {z - w[0] - w[1], z - w[1]};
   const int parts = parts_of(p, total), part = blockIdx.x / p.head_stride;
   st.total = total;
   st.parts = parts;
   st.b = -1;
   if (part >= parts) return;
-  const int64_t start = cut(total, parts, part), end = cut(total, parts, part + 1);
+  const int start = (int)((unsigned)total * (unsigned)part / (unsigned)parts);
+  const int end = (int)((unsigned)total * (unsigned)(part + 1) / (unsigned)parts);
   const bool in1 = before[1] <= start && start < before[1] + w[1];
   const bool in0 = before[0] <= start && start < before[0] + w[0];
   const int src = __ffs(__ballot_sync(0xffffffffu, in0 || in1)) - 1;
   const int k = __shfl_sync(0xffffffffu, (int)in1, src);
-  auto pick = [&](auto a0, auto a1) { return __shfl_sync(0xffffffffu, k ? a1 : a0, src); };
+  auto pick = [&](int a0, int a1) { return __shfl_sync(0xffffffffu, k ? a1 : a0, src); };
   st.b = 2 * src + k;
   st.raw = pick(raw[0], raw[1]);
   st.cu = pick(cu[0], cu[1]);
   st.s.seq = pick(s[0].seq, s[1].seq);
   st.s.kv = pick(s[0].kv, s[1].kv);
   st.s.tiles = pick(s[0].tiles, s[1].tiles);
-  int64_t tile = start - pick(before[0], before[1]);
-  const int64_t each = pick(per_head[0], per_head[1]);
+  int tile = start - pick(before[0], before[1]);
   st.line = start;
   st.left = end - start;
   st.h = blockIdx.x % p.head_stride;
   if (p.head_stride == 1) {
-    st.h = total < (1 << 24) ? (int)((unsigned)tile / (unsigned)each) : (int)(tile / each);
+    const int each = pick(per_head[0], per_head[1]);
+    st.h = (unsigned)tile / (unsigned)each;
     tile -= st.h * each;
   }
-  st.rt = find_row_tile<TK>(p, st.s, tile);
-  st.t0 = (int)(tile - tiles_before<TK>(p, st.s, st.rt));
+  st.rt = 0;
+  st.t0 = tile;
+  if (st.s.tiles > 1) {
+    st.rt = find_row_tile<TK>(p, st.s, tile);
+    st.t0 = tile - (int)tiles_before<TK>(p, st.s, st.rt);
+  }
 }
 
 // Every thread of the CTA scans the batch (kThreads sequences at a time); the results are in *st after the
@@ -460,77 +461,76 @@ __device__ __forceinline__ void load_f(const float* src, float (&v)[N]) {
 //   m = max_s m_s, O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
 // Other CTAs wrote them, so they are read past L1.  Latency is all it costs: the statistics and the first U segments'
 // values are fetched together, and the maps too.
-template <typename T, int D>
+template <typename T, int D, int MAPS>
 __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDesc& d, int first, int tok, int hh) {
   constexpr int NB = D == 256 ? 1 : 2;
   constexpr int N = D / 32;                   // columns per lane
-  constexpr int NW = (kGrid + 31) / 32;       // segment weights per lane
-  constexpr int U = D == 256 ? 4 : 8;         // segments in flight
+  constexpr int U = D == 256 || MAPS == 2 ? 4 : 8;  // segments in flight
   const int lane = threadIdx.x & 31;
-  const int maps = p.maps(), gh = p.group / maps;
+  const int gh = p.group / MAPS;
   const int col = lane * N;
-  const int token = d.token0 + tok, head = (d.kv_head * gh + hh) * maps;
+  const int token = d.token0 + tok, head = (d.kv_head * gh + hh) * MAPS;
   // segment s lies in CTA first + s * head_stride: in its slot 1 where the item starts, in slot 0 after that
-  int r[2] = {partial_row(p, d.two, tok, hh, 0), maps == 2 ? partial_row(p, d.two, tok, hh, 1) : 0};
-  auto prow = [&](int map, int s) { return ((int64_t)(first + s * p.head_stride) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r[map]; };
-  float2 ml[2][NW];
+  int r[MAPS];
 #pragma unroll
-  for (int map = 0; map < 2; ++map)
+  for (int map = 0; map < MAPS; ++map) r[map] = partial_row(p, d.two, tok, hh, map);
+  auto prow = [&](int map, int s) { return ((first + s * p.head_stride) * 2 + (s == 0 ? 1 : 0)) * (NB * 128) + r[map]; };
+  // a lane's statistics: of segments lane, lane + 32, ...
+  auto stat = [&](int map, int s) { return s < d.n_seg ? __ldcg(p.ml + prow(map, s)) : make_float2(-INFINITY, 0.f); };
+  float2 own[MAPS];
 #pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      const int s = k * 32 + lane;
-      ml[map][k] = make_float2(-INFINITY, 0.f);
-      if (map < maps && s < d.n_seg) ml[map][k] = __ldcg(p.ml + prow(map, s));
-    }
-  float v[2][U][N];
+  for (int map = 0; map < MAPS; ++map) own[map] = stat(map, lane);
+  float v[MAPS][U][N];
   auto fetch = [&](int s0) {
 #pragma unroll
-    for (int map = 0; map < 2; ++map)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (map < maps && s0 + u < d.n_seg && col < p.row) load_f<N>(p.part + prow(map, s0 + u) * D + col, v[map][u]);
+      for (int map = 0; map < MAPS; ++map)
+        if (s0 + u < d.n_seg && col < p.row) load_f<N>(p.part + (int64_t)prow(map, s0 + u) * D + col, v[map][u]);
   };
   fetch(0);
-  float wt[2][NW], top[2], sum[2], acc[2][N];
+  float top[MAPS], base[MAPS], sum[MAPS], acc[MAPS][N];
 #pragma unroll
-  for (int map = 0; map < 2; ++map) {
-    top[map] = -INFINITY;
-    sum[map] = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) top[map] = fmaxf(top[map], ml[map][k].x);
+  for (int map = 0; map < MAPS; ++map) {
+    top[map] = own[map].x;
+    for (int s = lane + 32; s < d.n_seg; s += 32) top[map] = fmaxf(top[map], stat(map, s).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top[map] = fmaxf(top[map], __shfl_xor_sync(0xffffffffu, top[map], o));
-    const float base = top[map] == -INFINITY ? 0.f : top[map];
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      wt[map][k] = fast_exp2(ml[map][k].x - base);
-      sum[map] = fmaf(ml[map][k].y, wt[map][k], sum[map]);
+    base[map] = top[map] == -INFINITY ? 0.f : top[map];
+    sum[map] = own[map].y * fast_exp2(own[map].x - base[map]);
+    for (int s = lane + 32; s < d.n_seg; s += 32) {
+      const float2 o = stat(map, s);
+      sum[map] = fmaf(o.y, fast_exp2(o.x - base[map]), sum[map]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum[map] += __shfl_xor_sync(0xffffffffu, sum[map], o);
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[map][i] = 0.f;
   }
+  float wt[MAPS];
+#pragma unroll 1
+  for (int s0 = 0; s0 < d.n_seg; s0 += U) {
+    if (s0 > 0) fetch(s0);
+    if (s0 % 32 == 0) {
 #pragma unroll
-  for (int k = 0; k < NW; ++k)
-    for (int s0 = k * 32; s0 < min(d.n_seg, k * 32 + 32); s0 += U) {
-      if (s0 > 0) fetch(s0);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int map = 0; map < 2; ++map) {
-          const float f = __shfl_sync(0xffffffffu, wt[map][k], (s0 + u) & 31);
-          if (map < maps && s0 + u < d.n_seg && col < p.row) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[map][i] = fmaf(f, v[map][u][i], acc[map][i]);
-          }
-        }
+      for (int map = 0; map < MAPS; ++map) wt[map] = fast_exp2((s0 == 0 ? own[map] : stat(map, s0 + lane)).x - base[map]);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int map = 0; map < MAPS; ++map) {
+        const float f = __shfl_sync(0xffffffffu, wt[map], (s0 + u) & 31);
+        if (s0 + u < d.n_seg && col < p.row) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[map][i] = fmaf(f, v[map][u][i], acc[map][i]);
+        }
+      }
+  }
   float y[N];
   const float inv = sum[0] > 0.f ? 1.f / sum[0] : 0.f;  // a row without keys gets 0
 #pragma unroll
   for (int i = 0; i < N; ++i) y[i] = acc[0][i] * inv;
-  if (maps == 2) {
+  if constexpr (MAPS == 2) {
     const float f = sum[1] > 0.f ? -p.lambda[head >> 1] / sum[1] : 0.f;
     float post = p.out_scale, ss = 0.f;
 #pragma unroll
@@ -554,11 +554,17 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
     uint32_t o[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1], (T*)nullptr);
-    T* dst = static_cast<T*>(p.out) + ((int64_t)token * (p.heads / maps) + head / maps) * p.row + col;
+    T* dst = static_cast<T*>(p.out) + ((int64_t)token * (p.heads / MAPS) + head / MAPS) * p.row + col;
     if constexpr (N == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
     else if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDesc& d, int first, int tok, int hh) {
+  if (p.maps() == 1) combine_row<T, D, 1>(p, d, first, tok, hh);
+  else combine_row<T, D, 2>(p, d, first, tok, hh);
 }
 
 // ---------------------------------------------------------------------------------------------- launches

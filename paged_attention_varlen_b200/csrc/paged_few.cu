@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   dependency_trigger();
   tc_fence_before();
   Start st;
-  if (p.batch <= 64) {
+  if (p.small) {
     find_start_small<128>(p, st);
     __syncthreads();
   } else {
@@ -610,7 +610,10 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
           const int q0 = st.part_of(tile0), n_seg = st.part_of(tile0 + w.n - 1) - q0 + 1;
           const int first = q0 * p.head_stride + (p.head_stride > 1 ? w.h : 0);
           const bool last = f.ok && atomicAdd(p.arrived + first, 1) == n_seg - 1;
-          if (last) p.arrived[first] = 0;  // for the next execution
+          if (last) {
+            p.arrived[first] = 0;  // for the next execution
+            __threadfence();
+          }
           const int k = w.t0 > 0 ? 0 : 1;
           tab.join[k] = PagedDesc{last ? n_seg : 0, (int)token0, tokens, w.h, w.rt * p.tb + off, 0};
           tab.first[k] = first;
@@ -620,7 +623,6 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     } while (w.next(p));
     // ---- the joins that fell to this CTA, both items' rows side by side (after the loop, so that what a join holds in
     // registers does not weigh on the tiles)
-    if (r == 0) __threadfence();
     named_barrier_sync(1, 256);
     const int n0 = tab.join[0].n_seg ? tab.join[0].tokens * group / maps : 0, n1 = tab.join[1].n_seg ? tab.join[1].tokens * group / maps : 0;
     for (int o = warp; o < n0 + n1; o += 8) {

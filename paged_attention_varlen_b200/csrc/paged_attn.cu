@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       mbar_wait(full_bar + (i % depth), (i / depth) & 1, status, is_k ? kDevTimeoutKFull : kDevTimeoutVFull);
     __syncwarp();
   } else if (warp == kWarpMma) {
-    // -------------------------------------------------------------- MMA issuer: one thread
-    if (lane == 0) {
+    // -------------------------------------------------------------- MMA issuer: a warp in step, one lane issues
+    const uint32_t lead = elect_one();
     const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_addr(sK), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_addr(sV), TK * 128, 1024);  // MN-major
@@ -339,39 +339,42 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, false, true, 128, (p.row + 15) & ~15);
     const bool per_map = p.maps() == 2;
     const int steps_row = (p.row + 15) / 16;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
+    };
     bool ok = true;
     uint32_t item = 0, sp0 = 0, sp1 = 0;
     uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // ring positions: slot and phase
     do {
-      const int cnt = w.t1 - w.t0;
-      const bool two = is_two();
+      const int cnt = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      const bool two = __any_sync(0xffffffffu, is_two());
       const int U = two ? 2 * cnt : cnt;
       auto issue_qk = [&](int u) -> bool {
         const int b = u & 1;
-        if ((!two || b == 0) && !mbar_wait(k_full + ks, kp, status, kDevTimeoutKFull)) return false;
+        if ((!two || b == 0) && !wait_all(k_full + ks, kp, kDevTimeoutKFull)) return false;
         // the buffer's previous P has been multiplied (before the item: q_full says so)
-        if (u >= 2 && !mbar_wait(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, status, kDevTimeoutODone)) return false;
+        if (u >= 2 && !wait_all(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, kDevTimeoutODone)) return false;
         tc_fence_after();
-        // the columns that hold q: a row's, or its map's where a block is a map
-        const int lo = two && per_map ? b * p.dq / 16 : 0;
-        const int hi = two && per_map ? ((b + 1) * p.dq + 15) / 16 : steps_row;
         const uint64_t a0 = dq + (two && b ? kQStep : 0), b0 = dk + ks * kStep;
         const uint32_t d = tmem + C::S_COL(b);
-        auto step = [&](int kk) {
+        auto step = [&](int kk, bool acc) {
           const uint32_t in = (kk % 4) * (32 >> 4);
-          mma_ss(d, a0 + ((kk / 4) * ((128 * 128) >> 4) + in), b0 + ((kk / 4) * ((TK * 128) >> 4) + in), kIdescQk, kk > lo, false);
+          mma_ss_by(lead, d, a0 + ((kk / 4) * ((128 * 128) >> 4) + in), b0 + ((kk / 4) * ((TK * 128) >> 4) + in), kIdescQk, acc);
         };
-        // (one unrolled loop with a condition on each step gave products of the wrong operands with nvcc 12.9)
-        if (lo == 0 && hi == D / 16) {
+        if (two && per_map) {  // the columns of the block's map alone
+          const int lo = b * p.dq / 16, hi = ((b + 1) * p.dq + 15) / 16;
+#pragma unroll 1
+          for (int kk = lo; kk < hi; ++kk) step(kk, kk > lo);
+        } else if (steps_row == D / 16) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) step(kk);
+          for (int kk = 0; kk < D / 16; ++kk) step(kk, kk > 0);
         } else {
 #pragma unroll 1
-          for (int kk = lo; kk < hi; ++kk) step(kk);
+          for (int kk = 0; kk < steps_row; ++kk) step(kk, kk > 0);
         }
-        mma_commit(s_full + b);
+        mma_commit_by(lead, s_full + b);
         if (!two || b == 1) {
-          mma_commit(k_empty + ks);
+          mma_commit_by(lead, k_empty + ks);
           if (++ks == NSK) {
             ks = 0;
             kp ^= 1;
@@ -380,45 +383,42 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         return true;
       };
       // Q is written after the previous item's last product, so the S buffers and O are free from here on
-      ok = mbar_wait(q_full, item & 1, status, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
+      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
       for (int u = 0; u < U && ok; ++u) {
         const int b = u & 1;
         const uint32_t ph = ((b ? sp1 : sp0) + (u >> 1)) & 1;
         const uint64_t v0 = dv + vs * kStep;
         const uint32_t o = tmem + C::O_COL(b), pcol = tmem + C::S_COL(b);
-        ok = ((two && b == 1) || mbar_wait(v_full + vs, vp, status, kDevTimeoutVFull)) &&
-             mbar_wait(p_lo + b, ph, status, kDevTimeoutPFull);
+        ok = ((two && b == 1) || wait_all(v_full + vs, vp, kDevTimeoutVFull)) && wait_all(p_lo + b, ph, kDevTimeoutPFull);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < TK / 32; ++kk)
-          mma_ts(o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u, false);
-        ok = mbar_wait(p_full + b, ph, status, kDevTimeoutPFull);
+          mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u);
+        ok = wait_all(p_full + b, ph, kDevTimeoutPFull);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = TK / 32; kk < TK / 16; ++kk)
-          mma_ts(o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, 1u, false);
-        mma_commit(pv_done + b);
+          mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, 1u);
+        mma_commit_by(lead, pv_done + b);
         if (!two || b == 1) {
-          mma_commit(v_empty + vs);
+          mma_commit_by(lead, v_empty + vs);
           if (++vs == NSV) {
             vs = 0;
             vp ^= 1;
           }
         }
-        if (u + NB >= U) mma_commit(o_done + (NB == 2 ? b : 0));
+        if (u + NB >= U) mma_commit_by(lead, o_done + (NB == 2 ? b : 0));
         if (u + 2 < U) ok = issue_qk(u + 2);
       }
       sp0 += (U + 1) >> 1;
       sp1 += U >> 1;
       ++item;
     } while (ok && w.next(p));
-    // all tensor-core work this thread issued has finished before TMEM is released
-    mma_commit(fin);
-    mbar_wait(fin, 0, status, kDevTimeoutFinal);
-    }
-    __syncwarp();
+    // all tensor-core work this warp issued has finished before TMEM is released
+    mma_commit_by(lead, fin);
+    wait_all(fin, 0, kDevTimeoutFinal);
   } else if (warp < kWarpK) {
     // -------------------------------------------------------------- softmax and epilogue
     if constexpr (NB == 2) regs_increase<216>();

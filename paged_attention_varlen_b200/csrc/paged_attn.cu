@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int NSK = D == 64 ? 5 : D == 128 ? 4 - NQ : 3;
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int SCRATCH = NQ * Q_BYTES;    // the Q buffers between items: what the joins pass through
-  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 4 * 2 + 2 + 1;
+  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 5 * 2 + 2 + 1;
   static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;  // 256 floats: sM
   static constexpr uint32_t S_COL(int b) { return b * TK; }
   static constexpr uint32_t O_COL(int b) { return 2 * TK + (NB == 2 ? b * D : 0); }
@@ -94,7 +94,7 @@ __device__ __forceinline__ void store_p(uint32_t col, const uint32_t (&pk)[N]) {
 
 // What a row keeps over an item.
 struct RowState {
-  float m, l;        // running max (log2 units; the one P is computed against) and sum
+  float m, l;        // running max (log2 units; the one P is computed against; kNoKey before any key) and sum
   int last_key;      // keys j <= last_key are allowed (-1: none)
   int pos;           // absolute position of the row's token
   float slope_log2;
@@ -146,7 +146,7 @@ __device__ __forceinline__ float scores(const PagedParams& p, const RowState& rs
 // Takes a tile's maximum into the running one.  Returns the factor that O and l must be rescaled by (1: none).
 __device__ __forceinline__ float grow(RowState& rs, float mx) {
   const float m_new = fmaxf(rs.m, mx);
-  if (!(m_new - rs.m > kRescaleThreshold)) return 1.f;  // so while both are -inf
+  if (!(m_new - rs.m > kRescaleThreshold)) return 1.f;
   const float alpha = fast_exp2(rs.m - m_new);
   rs.m = m_new;
   return alpha;
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   uint64_t* s_full = v_empty + NSV;  // [2] per S buffer
   uint64_t* p_lo = s_full + 2;       // [2] P of the tile's first half of keys written
   uint64_t* p_full = p_lo + 2;       // [2] all of P
-  uint64_t* pv_done = p_full + 2;    // [2]
+  uint64_t* lo_done = p_full + 2;    // [2] the product of P's first half
+  uint64_t* pv_done = lo_done + 2;   // [2]
   uint64_t* o_done = pv_done + 2;    // [2] per block: the item's last product
   uint64_t* fin = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       mbar_init(s_full + s, 1);
       mbar_init(p_lo + s, 128);
       mbar_init(p_full + s, 128);
+      mbar_init(lo_done + s, 1);
       mbar_init(pv_done + s, 1);
       mbar_init(o_done + s, 1);
     }
@@ -349,9 +351,10 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       const int cnt = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       const bool two = __any_sync(0xffffffffu, is_two());
       const int U = two ? 2 * cnt : cnt;
+      // K of step u has arrived (the second block finds its tile there)
+      auto wait_k = [&](int u) { return (two && (u & 1)) || wait_all(k_full + ks, kp, kDevTimeoutKFull); };
       auto issue_qk = [&](int u) -> bool {
         const int b = u & 1;
-        if ((!two || b == 0) && !wait_all(k_full + ks, kp, kDevTimeoutKFull)) return false;
         // the buffer's previous P has been multiplied (before the item: q_full says so)
         if (u >= 2 && !wait_all(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, kDevTimeoutODone)) return false;
         tc_fence_after();
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         return true;
       };
       // Q is written after the previous item's last product, so the S buffers and O are free from here on
-      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && issue_qk(0) && (U < 2 || issue_qk(1));
+      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && wait_k(0) && issue_qk(0) && (U < 2 || (wait_k(1) && issue_qk(1)));
       for (int u = 0; u < U && ok; ++u) {
         const int b = u & 1;
         const uint32_t ph = ((b ? sp1 : sp0) + (u >> 1)) & 1;
@@ -395,7 +398,8 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < TK / 32; ++kk)
           mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u);
-        ok = wait_all(p_full + b, ph, kDevTimeoutPFull);
+        mma_commit_by(lead, lo_done + b);
+        ok = (u + 2 >= U || wait_k(u + 2)) && wait_all(p_full + b, ph, kDevTimeoutPFull);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       }
       const int64_t token0 = w.cu + (int64_t)w.rt * p.tb, token = token0 + tok;
       RowState rs;
-      rs.m = -INFINITY;
+      rs.m = kNoKey;
       rs.l = 0.f;
       rs.pos = w.rt * p.tb + tok + off;
       rs.last_key = !valid ? -1 : p.mask_type == 0 ? w.s.kv - 1 : min(rs.pos, w.s.kv - 1);
@@ -515,48 +519,46 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
           __syncwarp();
           fence_proxy_async_smem();
         }
-        // With two blocks O is at rest here: the product before this one had to finish before S was written.
-        auto rescale = [&](float alpha) {
-          if (s == 0 || !__any_sync(0xffffffffu, alpha != 1.f)) return true;
-          if constexpr (NB == 1) {
-            if (!__all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((sb ? sp0 : sp1) + ((s - 1) >> 1)) & 1, status,
-                                                   kDevTimeoutODone)))
-              return false;
-            tc_fence_after();
-          }
-          scale_rows<D>(o_col, alpha);
-          return true;
-        };
-        auto half_done = [&](uint64_t* bar) {
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(bar);
-        };
-        uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
         if (warp_rows) {
-          // Half of the columns at a time, in 64 registers: the second half for its maximum, then the first for its
-          // maximum and its P, then the second again (P goes over the first half's scores only).
+          // The tile's halves, of which P V takes one after the other, in turn.  A half's P is computed against the
+          // running maximum as it stands, while its own maximum is found; only where that is more than 2^8 above,
+          // the maximum moves, O and l are rescaled and the half is computed again.
           constexpr int NC = TK / 2;
-          float x[NC];
-          load_cols<NC>(s_col + NC, x);
-          float mx = scores<NC>(p, rs, x, j0 + NC, raw_max);
-          load_cols<NC>(s_col, x);
-          mx = fmaxf(mx, scores<NC>(p, rs, x, j0, raw_max));
-          const float alpha = grow(rs, mx);
-          ok = rescale(alpha);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float x[NC];
+            load_cols<NC>(s_col + half * NC, x);
+            const float mx = scores<NC>(p, rs, x, j0 + half * NC, raw_max);
+            float alpha = 1.f;
+            if (s == 0 && half == 0) grow(rs, mx);  // nothing to rescale yet
+            uint32_t pk[NC / 2];
+            float sum;
+#pragma unroll 1
+            for (;;) {
+              uint64_t acc[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+              exponentials<T, NC>(x, scale2, f2pack(-rs.m, -rs.m), acc, pk);
+              sum = sum4(acc);
+              if (!__any_sync(0xffffffffu, mx - rs.m > kRescaleThreshold)) break;
+              alpha = grow(rs, mx);
+              // O must be at rest: after the product of the first half, or the tile before's (with two blocks S was
+              // only written after that)
+              if (half == 1)
+                ok = __all_sync(0xffffffffu, mbar_wait(lo_done + sb, ph & 1, status, kDevTimeoutODone));
+              else if (NB == 1)
+                ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((sb ? sp0 : sp1) + ((s - 1) >> 1)) & 1, status,
+                                                       kDevTimeoutODone));
+              if (!ok) break;
+              tc_fence_after();
+              scale_rows<D>(o_col, alpha);
+            }
+            if (!ok) break;
+            rs.l = rs.l * alpha + sum;
+            store_p<NC / 2>(s_col + half * (NC / 2), pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive((half ? p_full : p_lo) + sb);
+          }
           if (!ok) break;
-          const float base = rs.m == -INFINITY ? 0.f : rs.m;
-          const uint64_t negm2 = f2pack(-base, -base);
-          uint32_t pk[NC / 2];
-          exponentials<T, NC>(x, scale2, negm2, acc, pk);
-          store_p<NC / 2>(s_col, pk);
-          load_cols<NC>(s_col + NC, x);
-          half_done(p_lo + sb);
-          scores<NC>(p, rs, x, j0 + NC, raw_max);
-          exponentials<T, NC>(x, scale2, negm2, acc, pk);
-          store_p<NC / 2>(s_col + NC / 2, pk);
-          half_done(p_full + sb);
-          rs.l = rs.l * alpha + sum4(acc);
         } else {  // no row of the tile: what the lanes hold of P and O is read by nobody
           mbar_arrive(p_lo + sb);
           mbar_arrive(p_full + sb);
@@ -833,14 +835,21 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const Pa
 }
 
 template <typename T, int D>
-cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool few, bool two, cudaStream_t stream) {
-  if (few) return launch_paged_few(std::is_same_v<T, __half> ? kF16 : kBF16, D, tmK, tmV, p, stream);
+cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool two, cudaStream_t stream) {
   cudaError_t e;
   if constexpr (D == 256) e = launch_attn<T, D, 1>(tmK, tmV, p, stream);
   else if constexpr (D == 64) e = launch_attn<T, D, 2>(tmK, tmV, p, stream);
   else e = two ? launch_attn<T, D, 2>(tmK, tmV, p, stream) : launch_attn<T, D, 1>(tmK, tmV, p, stream);
   if (e != cudaSuccess) return e;
   return launch_dependent(paged_combine_kernel<T, D>, dim3(kGrid, kCombineY), 256, 0, stream, p);
+}
+
+cudaError_t launch_any(int32_t dtype, int D, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, bool two,
+                       cudaStream_t stream) {
+  const bool f16 = dtype == kF16;
+  if (D == 64) return f16 ? launch<__half, 64>(tmK, tmV, p, two, stream) : launch<__nv_bfloat16, 64>(tmK, tmV, p, two, stream);
+  if (D == 128) return f16 ? launch<__half, 128>(tmK, tmV, p, two, stream) : launch<__nv_bfloat16, 128>(tmK, tmV, p, two, stream);
+  return f16 ? launch<__half, 256>(tmK, tmV, p, two, stream) : launch<__nv_bfloat16, 256>(tmK, tmV, p, two, stream);
 }
 
 uint64_t align256(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -908,32 +917,46 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     p.dq = plan->d;
     p.row = plan->row;
     p.tb1 = 128 / p.group;
-    // Two blocks of rows where sequences have more than one block's on average (the lengths are on the device; any
-    // lengths run on either); at D = 64 there is room for both Q blocks and deep rings anyway.
-    const bool few = p.group <= kFewRows && plan->n_tokens * p.group <= (int64_t)40 * p.batch;
-    const bool two = D == 64 || (D == 128 && plan->n_tokens * p.group > (int64_t)128 * p.batch);
-    p.tb = few ? kFewRows / p.group : !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
-    p.box_rows = box;
-    // Few rows: where a kv head's row does not fill the lines that L2 and HBM move, neighbouring heads share them, so
-    // the heads run side by side (CTA c takes head c % kvHeadNum) and find them in L2.  Below 140 busy SMs that would
-    // cost more than it gives.  Measured with 8 kv heads: rows of 160 bytes 690 -> XXX us, of 128 bytes 391 -> XXX us.
-    const int parts = kGrid / p.kv_heads;
-    p.head_stride = few && plan->row * 2 % 256 != 0 && parts * p.kv_heads >= 140 ? p.kv_heads : 1;
-    {
-      const int tk = few || D != 256 ? 128 : 64;
-      const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
-      p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
-    }
     p.scale_log2 = plan->qk_scale * kLog2e;
     p.norm_eps = plan->norm_eps;
     p.out_scale = plan->out_scale;
-    const bool f16 = plan->dtype == ALA_F16;
-    if (D == 64)
-      e = f16 ? launch<__half, 64>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 64>(plan->tmK, plan->tmV, p, few, two, stream);
-    else if (D == 128)
-      e = f16 ? launch<__half, 128>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 128>(plan->tmK, plan->tmV, p, few, two, stream);
-    else
-      e = f16 ? launch<__half, 256>(plan->tmK, plan->tmV, p, few, two, stream) : launch<__nv_bfloat16, 256>(plan->tmK, plan->tmV, p, few, two, stream);
+    p.box_rows = box;
+    p.rows_min = 0;
+    p.rows_max = INT32_MAX;
+    auto set_small = [&](int tk) {
+      const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
+      p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
+    };
+    // Which kernels run follows from the tokens a sequence has on average, since its length is on the device; any
+    // lengths run on either.  Rows of at most 32 per kv head: the kernel for few rows alone, 1.5 to 2.5 times as fast
+    // there (16 decoding tokens of 16000 keys: XXX against XXX us).  More: each sequence on the kernel that suits its
+    // own rows, if there may be sequences of both kinds (4 or more; decoding rows beside chunks: XXX -> XXX us,
+    // and 3 us for a launch that finds nothing).
+    const int64_t rows = plan->n_tokens * p.group;
+    const bool can_few = p.group <= kFewRows, few = can_few && rows <= (int64_t)40 * p.batch;
+    const bool both = !few && can_few && p.batch >= 4;
+    if (few || both) {
+      if (both) p.rows_max = kFewRows;
+      p.tb = kFewRows / p.group;
+      // Where a kv head's row does not fill the lines that L2 and HBM move, neighbouring heads share them, so the heads
+      // run side by side (CTA c takes head c % kvHeadNum) and find them in L2.  Below 140 busy SMs that would cost
+      // more than it gives.  Measured with 8 kv heads: rows of 160 bytes 690 -> 434 us, of 128 bytes 391 -> 353 us.
+      const int parts = kGrid / p.kv_heads;
+      p.head_stride = plan->row * 2 % 256 != 0 && parts * p.kv_heads >= 140 ? p.kv_heads : 1;
+      set_small(128);
+      e = launch_paged_few(plan->dtype, D, plan->tmK, plan->tmV, p, stream);
+    }
+    if (!few && e == cudaSuccess) {
+      // Two blocks of rows where sequences have more than one block's on average; at D = 64 there is room for both Q
+      // blocks and deep rings anyway.
+      const bool two = D == 64 || (D == 128 && rows > (int64_t)128 * p.batch);
+      if (both) p.rows_min = kFewRows + 1;
+      p.rows_max = INT32_MAX;
+      p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
+      p.head_stride = 1;
+      set_small(D == 256 ? 64 : 128);
+      e = launch_any(plan->dtype, D, plan->tmK, plan->tmV, p, two, stream);
+    }
   }
   if (e != cudaSuccess) {
     snprintf(err, errlen, "kernel launch failed: %s", cudaGetErrorString(e));

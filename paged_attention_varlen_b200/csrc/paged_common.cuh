@@ -13,6 +13,7 @@ namespace ala {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
+constexpr float kNoKey = -3.0e38f;         // a running maximum before any key: below every score, and finite
 constexpr int kGrid = 148;                 // one CTA per SM of a B200
 
 // What a split item's first CTA leaves for the combine kernel.
@@ -43,6 +44,7 @@ struct PagedParams {
   int32_t dq, row;                 // query head size, elements of a K / V row
   int32_t box_rows;
   int32_t small;                   // at most 64 sequences whose lengths, whatever they are, make fewer than 2^24 tiles
+  int32_t rows_min, rows_max;      // sequences with rows (per kv head) outside this range are another launch's
   int32_t head_stride;             // 1: the line holds all kv heads; kv_heads: a line for each, CTA c on that of head c % kv_heads
   float scale_log2, norm_eps, out_scale;
 
@@ -101,7 +103,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t v, __half*) { return __half22
 // One sequence as the kernel takes it: lengths outside what the tensors hold are cut to it.  Keys stay below
 // 2^30 (the plan checks it), so all but sums over sequences or row tiles is 32-bit arithmetic.
 struct Seq {
-  int seq, kv, tiles;  // new tokens, keys, row tiles
+  int seq, kv, tiles;  // new tokens, keys, row tiles (0: nothing here for this launch)
 };
 
 __device__ __forceinline__ int clamp_len(const PagedParams& p, int len) { return min(max(len, 0), p.n_tokens); }
@@ -110,7 +112,8 @@ __device__ __forceinline__ Seq make_seq(const PagedParams& p, int64_t cu, int ra
   Seq s;
   s.seq = (int)max((int64_t)0, min((int64_t)raw, p.n_tokens - cu));
   s.kv = min(max(kv, 0), p.max_blocks * p.block_size);
-  s.tiles = s.seq <= p.tb ? s.seq > 0 : (int)((unsigned)(s.seq + p.tb - 1) / (unsigned)p.tb);
+  const int64_t rows = (int64_t)s.seq * p.group;
+  s.tiles = rows < p.rows_min || rows > p.rows_max ? 0 : s.seq <= p.tb ? s.seq > 0 : (int)((unsigned)(s.seq + p.tb - 1) / (unsigned)p.tb);
   return s;
 }
 
@@ -219,7 +222,7 @@ struct Walker {
           raw = clamp_len(p, len_next);
           s = make_seq(p, cu, raw, kv_next);
           fetch(p);
-        } while (s.seq == 0);
+        } while (s.tiles == 0);
       }
     }
     enter(p);
@@ -284,7 +287,7 @@ __device__ __forceinline__ void find_start_small(const PagedParams& p, Start& st
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     s[k] = make_seq(p, cu[k], raw[k], keys[k]);
-    per_head[k] = s[k].seq > 0 ? (int)tiles_before<TK>(p, s[k], s[k].tiles) : 0;
+    per_head[k] = s[k].tiles > 0 ? (int)tiles_before<TK>(p, s[k], s[k].tiles) : 0;
     w[k] = p.head_stride > 1 ? per_head[k] : per_head[k] * p.kv_heads;
     if (blockIdx.x == 0 && threadIdx.x < 32 && 2 * lane + k < p.batch && (s[k].seq != len[k] || s[k].kv != keys[k]))
       atomicCAS(p.status + 1, 0, kDevBadLength);
@@ -366,7 +369,7 @@ __device__ void find_start(const PagedParams& p, Start* st, int64_t* red) {
     cu = add(before, x - raw);
     cu0 = add(cu0, sum);
     s = make_seq(p, cu, raw, keys);
-    per_head = b < p.batch && s.seq > 0 ? tiles_before<TK>(p, s, s.tiles) : 0;
+    per_head = b < p.batch && s.tiles > 0 ? tiles_before<TK>(p, s, s.tiles) : 0;
     w = p.head_stride > 1 ? per_head : per_head * p.kv_heads;
     if (blockIdx.x == 0 && b < p.batch && (s.seq != len || s.kv != keys)) atomicCAS(p.status + 1, 0, kDevBadLength);
     int64_t z = w;

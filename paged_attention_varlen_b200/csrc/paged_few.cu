@@ -99,8 +99,6 @@ struct FewState {
   bool ok;
 };
 
-constexpr float kNoKey = -3.0e38f;
-
 // One item: its key tiles and its epilogue, R rows, RT of them this thread's.  After a failed wait a warp skips the waits that are left, but
 // goes through every tile and item, so that the warps meet as often as ever.
 template <typename T, int D, int R>
@@ -485,7 +483,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // -------------------------------------------------------------- MMA issuer: warp-uniform, one lane issues
-    const bool leader = elect_one();
+    const uint32_t lead = elect_one();
     const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_addr(ring), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_addr(ring), 128 * 128, 1024);  // V^T: the columns run along M
@@ -512,15 +510,12 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         if (!wait_all(full + slot, phase, kDevTimeoutKFull)) return false;
         tc_fence_after();
         const uint64_t a0 = dk + slot * kStep;
-        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + b * 32, a0 + (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2, dq + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2,
-                   idesc_qk, kk > 0, false);
-          mma_commit(s_full + b);
-          mma_commit(empty + slot);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_by(lead, tmem + b * 32, a0 + (kk / 4) * ((128 * 128) >> 4) + (kk % 4) * 2, dq + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2,
+                    idesc_qk, kk > 0);
+        mma_commit_by(lead, s_full + b);
+        mma_commit_by(lead, empty + slot);
         advance();
         return true;
       };
@@ -534,25 +529,21 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t a0 = dv + slot * kStep, b0 = dp + b * kPStep;
-        if (leader) {
 #pragma unroll
-          for (int mi = 0; mi < C::MT; ++mi)
+        for (int mi = 0; mi < C::MT; ++mi)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ss(tmem + C::O_COL + mi * 32, a0 + mi * ((2 * 128 * 128) >> 4) + kk * ((16 * 128) >> 4),
-                     b0 + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2, idesc_pv, (u > 0 || kk > 0) ? 1u : 0u, false);
-          mma_commit(empty + slot);
-          mma_commit(pv_done + b);
-          if (u == cnt - 1) mma_commit(o_done);
-        }
-        __syncwarp();
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss_by(lead, tmem + C::O_COL + mi * 32, a0 + mi * ((2 * 128 * 128) >> 4) + kk * ((16 * 128) >> 4),
+                      b0 + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2, idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_by(lead, empty + slot);
+        mma_commit_by(lead, pv_done + b);
+        if (u == cnt - 1) mma_commit_by(lead, o_done);
         advance();
       }
       ++item;
     } while (ok && w.next(p));
     // all tensor-core work this warp issued has finished before TMEM is released
-    if (leader) mma_commit(fin);
-    __syncwarp();
+    mma_commit_by(lead, fin);
     wait_all(fin, 0, kDevTimeoutFinal);
   } else {
     // -------------------------------------------------------------- softmax and epilogue

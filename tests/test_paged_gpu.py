@@ -117,6 +117,33 @@ def test_many_tiles_for_every_cta(maps, d):
     _check(c)
 
 
+def _grow(c, lens, backwards, block):
+    """Keys that grow along (or against) the sequence, so that the running maximum moves again and again."""
+    for b, (_, kv) in enumerate(lens):
+        blocks = c["tables"][b, :-(-kv // block)].long()
+        at = torch.arange(len(blocks) * block, dtype=torch.float32).view(-1, block, 1, 1) / max(kv, 1)
+        c["k"][blocks] = c["k"][blocks] * ((1 - at).clamp(min=0) if backwards else at).mul(30).to(c["k"].dtype)
+
+
+@pytest.mark.parametrize("backwards", [False, True])
+@pytest.mark.parametrize("lens,heads,kv_heads,d,maps", [
+    ([(1, 1300), (1, 700)], 4, 1, 128, 1), ([(2, 1300), (1, 64)], 12, 2, 64, 1), ([(5, 900)], 5, 1, 80, 1), ([(1, 900)], 32, 1, 256, 1),
+    ([(40, 700), (1, 300)], 4, 2, 128, 1), ([(40, 700), (33, 500)], 4, 2, 64, 1), ([(50, 600)], 2, 1, 256, 1),
+    ([(300, 900), (1, 200)], 4, 2, 128, 1), ([(1, 700), (2, 300)], 4, 1, 64, 2), ([(150, 600)], 4, 2, 32, 2), ([(60, 400)], 2, 1, 128, 2)])
+def test_a_running_maximum_that_keeps_moving(lens, heads, kv_heads, d, maps, backwards):
+    c = paged_ref.make_case(lens, heads, kv_heads, d, BF, 64, 9, 470 + d, maps=maps)
+    _grow(c, lens, backwards, 64)
+    _check(c)
+
+
+@pytest.mark.parametrize("d,maps", [(64, 1), (128, 1), (256, 1), (32, 2), (64, 2), (128, 2)])
+def test_decoding_rows_beside_chunks(d, maps):
+    # sequences of few rows and of many in one batch: two launches share the work
+    rng = random.Random(d)
+    lens = [(1, rng.randint(1, 900)) for _ in range(9)] + [(150, 400), (0, 70), (3, 333), (200, 200), (40, 1000), (1, 2)]
+    _check(paged_ref.make_case(lens, 8, 2, d, BF, 32, 9, 480 + d, maps=maps, tail=3, norm=True))
+
+
 @pytest.mark.parametrize("n,kv", [(1, 1), (1, 2), (2, 2), (127, 127), (128, 128), (129, 640), (1, 128), (1, 129)])
 def test_single_sequences(n, kv):
     for d in (64, 128, 256):

@@ -145,6 +145,8 @@ int ala::paged_plan(PagedPlan* plan, const PagedAttnArgs& a, char* errbuf, size_
     if (nb == 0) return fail(ALA_INVALID_SHAPE, "the cache has no blocks");
     if (!aligned(a.query->data, 16) || !aligned(a.key->data, 16) || !aligned(a.value->data, 16))
       return fail(ALA_INVALID_PARAM, "query, key and value must be 16-byte aligned");
+    for (const ala_tensor* t : {a.block_tables, a.seq_len, a.kv_seq_len, a.slopes, a.lambda, a.norm_weight, a.lse})
+      if (t && !aligned(t->data, 4)) return fail(ALA_INVALID_PARAM, "a tensor is not aligned to its elements");
     if (!aligned(a.out->data, 32)) return fail(ALA_INVALID_PARAM, "attnOut must be 32-byte aligned");
   }
   auto f32 = [](const ala_tensor* t) { return t ? static_cast<const float*>(t->data) : nullptr; };
@@ -216,6 +218,7 @@ extern "C" int ala_paged_step(const ala_tensor* seqLen, const ala_tensor* contex
     int64_t n = 1;
     for (int i = 0; i < t->ndim; ++i) n *= t->dims[i] > kMaxKeys ? kMaxKeys : t->dims[i];
     if (n > 0 && !t->data) return fail(ALA_NULL_REQUIRED, "a tensor has a NULL data pointer");
+    if (!aligned(t->data, 4)) return fail(ALA_INVALID_PARAM, "a tensor is not aligned to its elements");
   }
   if (blockSize <= 0) return fail(ALA_INVALID_PARAM, "blockSize must be > 0 (got %d)", blockSize);
   if (blockTables->ndim != 2) return fail(ALA_INVALID_SHAPE, "blockTables must be [batch, maxBlockNum]");
@@ -325,6 +328,7 @@ extern "C" int ala_paged_write(const ala_tensor* key, int64_t keyStride, const a
   if (value && (blocks[0] != blocks[1] || block_size[0] != block_size[1]))
     return fail(ALA_INVALID_SHAPE, "the key and value caches differ in blocks");
   if (n > 0 && !slotMapping->data) return fail(ALA_NULL_REQUIRED, "slotMapping has a NULL data pointer");
+  if (!aligned(slotMapping->data, 4)) return fail(ALA_INVALID_PARAM, "slotMapping is not aligned to its elements");
   a.key = static_cast<const uint8_t*>(key->data);
   a.value = value ? static_cast<const uint8_t*>(value->data) : nullptr;
   a.key_cache = static_cast<uint8_t*>(keyCache->data);

@@ -167,3 +167,41 @@ def test_python_refuses_tensors_on_different_devices():
         _attn(seq_len=meta)
     with pytest.raises(ValueError):
         ala.plan_paged_write(_kv, _kv, _i32(4), torch.zeros(3, 16, 48), torch.zeros(3, 16, 48, device="meta"))
+
+
+def _odd(shape, dtype):
+    """A tensor whose address is one byte off its elements' alignment."""
+    t = ala.AlaTensor()
+    buf = (ctypes.c_uint8 * 4096)()
+    t.data = (ctypes.addressof(buf) // 8 + 1) * 8 + 1
+    t.dtype, t.ndim = dtype, len(shape)
+    for i, s in enumerate(shape):
+        t.dims[i] = s
+    t._buf = buf
+    return t
+
+
+@pytest.mark.parametrize("name,shape", [("seqLen", (3,)), ("blockTables", (3, 4)), ("status", (1,)), ("slotMapping", (12,))])
+def test_step_refuses_an_address_off_its_elements(name, shape):
+    ts = {k: x if isinstance(x, int) else ala.tensor(x) for k, x in _step_args().items()}
+    ts[name] = _odd(shape, ala.I32)
+    assert ala.lib().ala_paged_step(*[x if isinstance(x, int) else ctypes.byref(x) for x in ts.values()], None) == 4
+
+
+@pytest.mark.parametrize("which", ["tables", "seq", "kv", "lse", "slots"])
+def test_attention_and_write_refuse_an_address_off_its_elements(which):
+    L = ala.lib()
+    if which == "slots":
+        ts = [ala.tensor(_kv), ala.tensor(_kv), _odd((4,), ala.I32), ala.tensor(torch.zeros(3, 16, 2, 24)), ala.tensor(torch.zeros(3, 16, 48))]
+        r = [ctypes.byref(t) for t in ts]
+        assert L.ala_paged_write(r[0], 0, r[1], 0, r[2], r[3], r[4], None) == 4
+        return
+    q, k, v, out = _aligned(10, 8, 64), _aligned(6, 16, 2, 64), _aligned(6, 16, 2, 64), _aligned(10, 8, 64)
+    ts = dict(tables=ala.tensor(_i32(3, 4)), seq=ala.tensor(_i32(3)), kv=ala.tensor(_i32(3)), lse=ala.tensor(torch.zeros(10, 8)))
+    ts[which] = _odd({"tables": (3, 4), "lse": (10, 8)}.get(which, (3,)), ala.F32 if which == "lse" else ala.I32)
+    tq, tk, tv, to = (ala.tensor(x) for x in (q, k, v, out))
+    ws, h = ctypes.c_uint64(0), ctypes.c_void_p(0)
+    b = ctypes.byref
+    st = L.ala_paged_attention_get_workspace_size(b(tq), 0, b(tk), b(tv), b(ts["tables"]), b(ts["seq"]), b(ts["kv"]), None, 9, 8, 2, 0.1,
+                                                  b(to), b(ts["lse"]), b(ws), b(h))
+    assert st == 4 and not h.value

@@ -274,6 +274,48 @@ def test_bad_blocks_and_lengths_are_reported_and_read_nothing():
     _compare(c, out, lse)
 
 
+@pytest.mark.parametrize("lens,d", [([(1, 3000), (2, 900)], 128), ([(90, 400), (1, 50)], 64)])
+def test_an_unbound_workspace_may_hold_anything(lens, d):
+    c = paged_ref.make_case(lens, 8, 2, d, BF, 64, 9, 930 + d)
+    op, out, lse = _plan(c)
+    ws = torch.full((op.workspace_size,), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        out.fill_(7.0)
+        assert ala.lib().ala_paged_attention(ws.data_ptr(), op.workspace_size, op._handle, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        _compare(c, out, lse)
+    # bound by hand, and unbound again
+    assert ala.lib().ala_op_bind_workspace(op._handle, ws.data_ptr(), op.workspace_size, None) == 0
+    assert ala.lib().ala_paged_attention(ws.data_ptr(), op.workspace_size, op._handle, torch.cuda.current_stream().cuda_stream) == 0
+    assert ala.lib().ala_op_bind_workspace(op._handle, None, 0, None) == 0
+    torch.cuda.synchronize()
+    _compare(c, out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_rows_past_four_gigabytes_of_cache(n):
+    # a cache of 5 GiB whose last pages hold the sequence; what lies before them is never touched
+    block, heads, d = 64, 8, 128
+    blocks = (5 << 30) // (block * heads * d * 2)
+    small = paged_ref.make_case([(n, 300)], 16, heads, d, BF, block, 9, 940)
+    k = torch.empty(blocks, block, heads, d, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    # the rows go in through the write, slot by slot
+    used = small["tables"][0, :5].long()
+    far = torch.arange(blocks - 5, blocks)
+    slots = torch.cat([b * block + torch.arange(block) for b in far])[:300].to(torch.int32).cuda()
+    rows = lambda x: x[used].flatten(0, 1)[:300].contiguous().cuda()  # noqa: E731
+    ala.paged_write(rows(small["k"]), rows(small["v"]), slots, k, v)
+    tables = far.to(torch.int32).view(1, -1).cuda()
+    out = torch.full((n, 16, d), 7.0, dtype=BF, device="cuda")
+    op, _ = ala.plan_paged_attention(small["q"].cuda(), k, v, tables, small["seq"].cuda(), small["kv"].cuda(), 9, 16, heads,
+                                     small["scale"], out=out)
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    _compare(small, out, None)
+
+
 # ---------------------------------------------------------------------------------------------- step and write
 
 def _step_case(rng, batch, width, block, ended=True):

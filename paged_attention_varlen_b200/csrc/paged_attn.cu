@@ -63,14 +63,17 @@ struct Cfg {
   static constexpr int NSK = D == 64 ? 5 : D == 128 ? 4 - NQ : 3;
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int SCRATCH = NQ * Q_BYTES;    // the Q buffers between items: what the joins pass through
-  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 5 * 2 + 2 + 1;
+  // S buffers.  A third, where tensor memory has room for it, takes the scores of a block's next tile while the block's
+  // softmax still works on this one: chunks of D = 64 440 -> XXX us.
+  static constexpr int NBUF = D == 64 ? 3 : 2;
+  static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 5 * NBUF + 2 + 1;
   static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;  // 256 floats: sM
-  static constexpr uint32_t S_COL(int b) { return b * TK; }
-  static constexpr uint32_t O_COL(int b) { return 2 * TK + (NB == 2 ? b * D : 0); }
+  static constexpr uint32_t S_COL(int k) { return k * TK; }
+  static constexpr uint32_t O_COL(int b) { return NBUF * TK + (NB == 2 ? b * D : 0); }
   static constexpr uint32_t TMEM_COLS = 512;
   static_assert(SMEM + 512 <= 232448, "shared memory budget (512: the static part)");
   static_assert(SCRATCH / (NB * 4 * 32 * 4) % 32 == 0, "the joins take 32 columns at a time");
-  static_assert(2 * TK + NB * D <= TMEM_COLS, "tensor memory budget");
+  static_assert(NBUF * TK + NB * D <= TMEM_COLS, "tensor memory budget");
 };
 
 // ---------------------------------------------------------------------------------------------- softmax
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p) {
   using C = Cfg<T, D, NQ>;
-  constexpr int TK = C::TK, NSK = C::NSK, NSV = C::NSV, NB = C::NB;
+  constexpr int TK = C::TK, NSK = C::NSK, NSV = C::NSV, NB = C::NB, NBUF = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                        // [NQ][Q_BYTES]; between items the scratch of the joins
@@ -210,12 +213,12 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   uint64_t* k_empty = k_full + NSK;
   uint64_t* v_full = k_empty + NSK;
   uint64_t* v_empty = v_full + NSV;
-  uint64_t* s_full = v_empty + NSV;  // [2] per S buffer
-  uint64_t* p_lo = s_full + 2;       // [2] P of the tile's first half of keys written
-  uint64_t* p_full = p_lo + 2;       // [2] all of P
-  uint64_t* lo_done = p_full + 2;    // [2] the product of P's first half
-  uint64_t* pv_done = lo_done + 2;   // [2]
-  uint64_t* o_done = pv_done + 2;    // [2] per block: the item's last product
+  uint64_t* s_full = v_empty + NSV;     // [NBUF] per S buffer
+  uint64_t* p_lo = s_full + NBUF;       // [NBUF] P of the tile's first half of keys written
+  uint64_t* p_full = p_lo + NBUF;       // [NBUF] all of P
+  uint64_t* lo_done = p_full + NBUF;    // [NBUF] the product of P's first half
+  uint64_t* pv_done = lo_done + NBUF;   // [NBUF]
+  uint64_t* o_done = pv_done + NBUF;    // [2] per block: the item's last product
   uint64_t* fin = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   __shared__ Start st;
@@ -236,14 +239,15 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       mbar_init(v_full + s, 1);
       mbar_init(v_empty + s, 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < NBUF; ++s) {
       mbar_init(s_full + s, 1);
       mbar_init(p_lo + s, 128);
       mbar_init(p_full + s, 128);
       mbar_init(lo_done + s, 1);
       mbar_init(pv_done + s, 1);
-      mbar_init(o_done + s, 1);
     }
+    mbar_init(o_done, 1);
+    mbar_init(o_done + 1, 1);
     mbar_init(fin, 1);
     fence_mbar_init();
   }
@@ -266,10 +270,21 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   Walker<TK> w;
   w.begin(p, st);
 
-  // An item of cnt tiles is U steps: step u fills S buffer u & 1 and multiplies its P.  With two blocks of rows,
+  // An item of cnt tiles is U steps: step u fills S buffer u % NBUF and multiplies its P.  With two blocks of rows,
   // steps 2i and 2i + 1 are tile i for block 0 and 1; otherwise step u is tile u, for block u & 1 of the two that
   // hold the same rows (NB = 1: for the one block).  Ring phases run on across items by a counter of tiles (slot
   // g % depth, phase g / depth), those of a buffer by its count of steps, q_full and o_done by items.
+  uint32_t used[NBUF] = {};  // steps of each S buffer in the items before
+  auto phase_of = [&](int u) {  // of step u's buffer
+    uint32_t c = used[0];
+    if (NBUF == 3 ? u % 3 == 1 : (u & 1)) c = used[1];
+    if (NBUF == 3 && u % 3 == 2) c = used[NBUF - 1];
+    return (c + u / NBUF) & 1;
+  };
+  auto count_steps = [&](int U) {
+#pragma unroll
+    for (int k = 0; k < NBUF; ++k) used[k] += (U - k + NBUF - 1) / NBUF;
+  };
   auto is_two = [&]() { return NQ == 2 && w.tokens(p) * p.group > 128; };
   // register split for NB = 2: the softmax warps take 216 each, the others keep 72 (256 * 216 + 128 * 72 =
   // 64512 = 384 * 168, all that the block is launched with)
@@ -345,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
     };
     bool ok = true;
-    uint32_t item = 0, sp0 = 0, sp1 = 0;
+    uint32_t item = 0;
     uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // ring positions: slot and phase
     do {
       const int cnt = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
@@ -354,12 +369,12 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       // K of step u has arrived (the second block finds its tile there)
       auto wait_k = [&](int u) { return (two && (u & 1)) || wait_all(k_full + ks, kp, kDevTimeoutKFull); };
       auto issue_qk = [&](int u) -> bool {
-        const int b = u & 1;
+        const int b = u & 1, k = u % NBUF;
         // the buffer's previous P has been multiplied (before the item: q_full says so)
-        if (u >= 2 && !wait_all(pv_done + b, ((b ? sp1 : sp0) + (u >> 1) - 1) & 1, kDevTimeoutODone)) return false;
+        if (u >= NBUF && !wait_all(pv_done + k, phase_of(u - NBUF), kDevTimeoutODone)) return false;
         tc_fence_after();
         const uint64_t a0 = dq + (two && b ? kQStep : 0), b0 = dk + ks * kStep;
-        const uint32_t d = tmem + C::S_COL(b);
+        const uint32_t d = tmem + C::S_COL(k);
         auto step = [&](int kk, bool acc) {
           const uint32_t in = (kk % 4) * (32 >> 4);
           mma_ss_by(lead, d, a0 + ((kk / 4) * ((128 * 128) >> 4) + in), b0 + ((kk / 4) * ((TK * 128) >> 4) + in), kIdescQk, acc);
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
 #pragma unroll 1
           for (int kk = 0; kk < steps_row; ++kk) step(kk, kk > 0);
         }
-        mma_commit_by(lead, s_full + b);
+        mma_commit_by(lead, s_full + k);
         if (!two || b == 1) {
           mma_commit_by(lead, k_empty + ks);
           if (++ks == NSK) {
@@ -386,26 +401,28 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         return true;
       };
       // Q is written after the previous item's last product, so the S buffers and O are free from here on
-      ok = wait_all(q_full, item & 1, kDevTimeoutQ) && wait_k(0) && issue_qk(0) && (U < 2 || (wait_k(1) && issue_qk(1)));
+      ok = wait_all(q_full, item & 1, kDevTimeoutQ);
+      for (int u = 0; u < NBUF && u < U && ok; ++u) ok = wait_k(u) && issue_qk(u);
       for (int u = 0; u < U && ok; ++u) {
         const int b = u & 1;
-        const uint32_t ph = ((b ? sp1 : sp0) + (u >> 1)) & 1;
+        const int k = u % NBUF;
+        const uint32_t ph = phase_of(u);
         const uint64_t v0 = dv + vs * kStep;
-        const uint32_t o = tmem + C::O_COL(b), pcol = tmem + C::S_COL(b);
-        ok = ((two && b == 1) || wait_all(v_full + vs, vp, kDevTimeoutVFull)) && wait_all(p_lo + b, ph, kDevTimeoutPFull);
+        const uint32_t o = tmem + C::O_COL(b), pcol = tmem + C::S_COL(k);
+        ok = ((two && b == 1) || wait_all(v_full + vs, vp, kDevTimeoutVFull)) && wait_all(p_lo + k, ph, kDevTimeoutPFull);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < TK / 32; ++kk)
           mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u);
-        mma_commit_by(lead, lo_done + b);
-        ok = (u + 2 >= U || wait_k(u + 2)) && wait_all(p_full + b, ph, kDevTimeoutPFull);
+        mma_commit_by(lead, lo_done + k);
+        ok = (u + NBUF >= U || wait_k(u + NBUF)) && wait_all(p_full + k, ph, kDevTimeoutPFull);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = TK / 32; kk < TK / 16; ++kk)
           mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, 1u);
-        mma_commit_by(lead, pv_done + b);
+        mma_commit_by(lead, pv_done + k);
         if (!two || b == 1) {
           mma_commit_by(lead, v_empty + vs);
           if (++vs == NSV) {
@@ -414,10 +431,9 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
           }
         }
         if (u + NB >= U) mma_commit_by(lead, o_done + (NB == 2 ? b : 0));
-        if (u + 2 < U) ok = issue_qk(u + 2);
+        if (u + NBUF < U) ok = issue_qk(u + NBUF);
       }
-      sp0 += (U + 1) >> 1;
-      sp1 += U >> 1;
+      count_steps(U);
       ++item;
     } while (ok && w.next(p));
     // all tensor-core work this warp issued has finished before TMEM is released
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     const int group = p.group, maps = p.maps(), gh = group / maps;
     const bool raw_max = (p.mask_type == 0 || p.mask_type == 9) && p.scale_log2 > 0.f;  // scale folded into the exponent
     const uint64_t scale2 = raw_max ? f2pack(p.scale_log2, p.scale_log2) : f2pack(1.f, 1.f);
-    uint32_t g0 = 0, sp0 = 0, sp1 = 0, items = 0;  // tiles, steps of the S buffers, items that this block took part in
+    uint32_t g0 = 0, items = 0;  // tiles; items that this block took part in
     bool owner = false;
     // After a failed wait a warp skips what is left of the tiles, but goes on through the items, so that the
     // warps meet as often as ever.
@@ -495,12 +511,13 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
       // ---- key tiles, from the last
       const bool warp_rows = __any_sync(0xffffffffu, valid);
       for (int s = 0; s < steps && ok; ++s) {
-        const int sb = NB == 2 ? blk : s & 1;  // S buffer
-        const uint32_t ph = NB == 2 ? sp0 + s : (sb ? sp1 : sp0) + (s >> 1);
+        const int u = NB == 2 ? 2 * s + blk : s;  // step of the item
+        const int sb = u % NBUF;                  // its S buffer
+        const uint32_t ph = phase_of(u);
         const int i = NB == 1 || two ? s : 2 * s + blk;  // tile of the item
         const int j0 = (w.t1 - 1 - i) * TK;
         const uint32_t s_col = tmem + lanes + C::S_COL(sb);
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, ph & 1, status, kDevTimeoutSFull));
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, ph, status, kDevTimeoutSFull));
         if (!ok) break;
         tc_fence_after();
         if (s == 0 && blk == 0 && j0 + TK > w.s.kv) {
@@ -540,13 +557,10 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
               sum = sum4(acc);
               if (!__any_sync(0xffffffffu, mx - rs.m > kRescaleThreshold)) break;
               alpha = grow(rs, mx);
-              // O must be at rest: after the product of the first half, or the tile before's (with two blocks S was
-              // only written after that)
-              if (half == 1)
-                ok = __all_sync(0xffffffffu, mbar_wait(lo_done + sb, ph & 1, status, kDevTimeoutODone));
-              else if (NB == 1)
-                ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((sb ? sp0 : sp1) + ((s - 1) >> 1)) & 1, status,
-                                                       kDevTimeoutODone));
+              // O must be at rest: after the product of the first half, or of the block's step before
+              const int before = NB == 2 ? u - 2 : u - 1;
+              ok = __all_sync(0xffffffffu, half == 1 ? mbar_wait(lo_done + sb, ph, status, kDevTimeoutODone)
+                                                     : mbar_wait(pv_done + (before + NBUF) % NBUF, phase_of(before), status, kDevTimeoutODone));
               if (!ok) break;
               tc_fence_after();
               scale_rows<D>(o_col, alpha);
@@ -565,12 +579,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         }
       }
       g0 += cnt;
-      if constexpr (NB == 2) {
-        sp0 += steps;
-      } else {
-        sp0 += (steps + 1) >> 1;
-        sp1 += steps >> 1;
-      }
+      count_steps(two ? 2 * cnt : cnt);
       // o_done has one phase per item that the block took part in and is waited for once in each, so no wait can
       // meet the phase before or after its own
       if (steps > 0) {

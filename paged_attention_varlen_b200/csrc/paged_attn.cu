@@ -356,9 +356,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, false, true, 128, (p.row + 15) & ~15);
     const bool per_map = p.maps() == 2;
     const int steps_row = (p.row + 15) / 16;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
-    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) { return wait_warp(bar, parity, status, code); };
     bool ok = true;
     uint32_t item = 0;
     uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // ring positions: slot and phase
@@ -409,14 +407,16 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
         const uint32_t ph = phase_of(u);
         const uint64_t v0 = dv + vs * kStep;
         const uint32_t o = tmem + C::O_COL(b), pcol = tmem + C::S_COL(k);
-        ok = ((two && b == 1) || wait_all(v_full + vs, vp, kDevTimeoutVFull)) && wait_all(p_lo + k, ph, kDevTimeoutPFull);
+        ok = two && b == 1 ? wait_all(p_lo + k, ph, kDevTimeoutPFull)
+                           : wait_warp2(v_full + vs, vp, kDevTimeoutVFull, p_lo + k, ph, kDevTimeoutPFull, status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < TK / 32; ++kk)
           mma_ts_by(lead, o, pcol + kk * 8, v0 + ((kk * 16 * 128) >> 4), idesc_pv, (u >= NB || kk > 0) ? 1u : 0u);
         mma_commit_by(lead, lo_done + k);
-        ok = (u + NBUF >= U || wait_k(u + NBUF)) && wait_all(p_full + k, ph, kDevTimeoutPFull);
+        ok = u + NBUF >= U || (two && ((u + NBUF) & 1)) ? wait_all(p_full + k, ph, kDevTimeoutPFull)
+                                                        : wait_warp2(k_full + ks, kp, kDevTimeoutKFull, p_full + k, ph, kDevTimeoutPFull, status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll

@@ -570,6 +570,21 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
   else combine_row<T, D, 2>(p, d, first, tok, hh);
 }
 
+// ---------------------------------------------------------------------------------------------- waits of a warp in step
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status, int code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
+}
+// Two barriers at once: a wait that finds its phase over still costs some 150 cycles, and the issuing warp has six for
+// every tile of a block.
+__device__ __forceinline__ bool wait_warp2(uint64_t* bar0, uint32_t parity0, int code0, uint64_t* bar1, uint32_t parity1, int code1,
+                                           int* status) {
+  const bool first = mbar_test_wait(bar0, parity0), second = mbar_try_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, first && second)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar0, parity0, status, code0)) && __all_sync(0xffffffffu, mbar_wait(bar1, parity1, status, code1));
+}
+
 // ---------------------------------------------------------------------------------------------- launches
 
 // Every kernel here is a programmatic dependent launch: it is scheduled while the one before it on the stream ends,

@@ -489,9 +489,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     const uint64_t dv = smem_desc_sw128(smem_addr(ring), 128 * 128, 1024);  // V^T: the columns run along M
     const uint64_t dp = smem_desc_sw128(smem_addr(sP), 16, 1024);
     constexpr uint64_t kStep = C::KV_BYTES >> 4, kPStep = C::P_BYTES >> 4;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code));
-    };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, int code) { return wait_warp(bar, parity, status, code); };
     uint32_t slot = 0, phase = 0;
     auto advance = [&]() {
       if (++slot == NS) {
@@ -525,7 +523,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         const uint32_t b = g & 1;
         // S of the next tile goes over that of the last one, which has been read: its P has come
         if (u + 1 < cnt && !(ok = issue_qk(b ^ 1))) break;
-        ok = wait_all(full + slot, phase, kDevTimeoutVFull) && wait_all(p_full + b, (g >> 1) & 1, kDevTimeoutPFull);
+        ok = wait_warp2(full + slot, phase, kDevTimeoutVFull, p_full + b, (g >> 1) & 1, kDevTimeoutPFull, status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t a0 = dv + slot * kStep, b0 = dp + b * kPStep;

@@ -5,22 +5,18 @@
 //   O[t, h] = sum_j (softmax_j(s1) - lambda_h softmax_j(s2)) v_j, s_m = qkScale q[t, 2h + m] . k_(m),j
 //             and then, optionally, O <- O * rsqrt(mean(O^2) + eps) * w               (ala_paged_diff_attention)
 //
+// This kernel is for many query rows of a kv head, paged_few.cu for up to 32 (paged_run says which runs when).
+//
 // Rows.  The queries of one kv head are packed (token, head of the group), so that K / V are read once for the
 // group.  An item is the rows of up to two blocks of 128 (one at D = 256, whose O leaves no room in tensor
 // memory for a second) against one kv head's keys, in tiles of 128 keys (64 at D = 256).
 //   two blocks    more than 128 rows: every tile serves both blocks, and one block's products run while the
 //                 other's softmax does
-//   alternating   up to 128 rows: the blocks are the same rows, and take the tiles in turn; joined at the end
-//   quarters      up to 32 rows, alternating too: the rows are repeated in the four lane quarters of a block,
-//                 quarter w takes a quarter of each tile's keys (P is zero on the others), so that all the
-//                 softmax warps share the exponentials of a single token.  With 16 rows or fewer, the upper
-//                 lanes of a quarter carry what rounding P to 16 bits dropped: P V is then exact to 2^-17 or
-//                 so and costs no further product.
+//   in turns      up to 128 rows: the blocks are the same rows, and take the tiles in turn; joined at the end
 //
 // Differential attention is the same kernel over K rows [k1 | k2] of 2d elements, as they lie in the cache:
 // the query row of map 1 is [q1 | 0], that of map 2 is [0 | q2].  With two blocks a block is a map, and its
-// score product runs over that map's half alone; otherwise the two maps of a head are neighbouring rows, and
-// the zeros cost a decoding step nothing, since it is bound by the bytes of the cache.
+// score product runs over that map's half alone; otherwise the two maps of a head are neighbouring rows.
 //
 // Work split.  All key tiles of all (sequence, kv head, row tile) items form one line; CTA c of G takes the
 // tiles [c T / G, (c + 1) T / G).  A CTA finds its start by a scan over the batch and a search inside one
@@ -35,6 +31,12 @@
 //   then a warp each      TMA producer of the K ring, of the V ring (lane i gathers box i of a tile through
 //                         the block table), and the tcgen05 issuer: S_b = Q K^T, O_b += P_b V with P_b read
 //                         from TMEM over S_b, P V in two halves of the keys
+//
+// What bounds it: a block's chain of softmax (some 2900 cycles for 128 keys, of which 1024 to 2048 are ex2, the tensor
+// pipe's 512 to 1024 aside) and, with two S buffers, P V and the next Q K^T (1700).  The two blocks overlap; tensor
+// pipe and ex2 unit both run at 37 % of their cycles (2 x 2048 new tokens over 8000 keys), DRAM at 4 %.
+// Measured: 3 chunks of up to 4096 over 20000 keys, 32 / 8 heads, d 128: 2.24 to 2.6 ms, 820 to 960 TFLOP/s, by the
+// clock that the power cap leaves.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -64,7 +66,7 @@ struct Cfg {
   static constexpr int NSV = D == 64 ? 6 : D == 128 ? 3 : 2;
   static constexpr int SCRATCH = NQ * Q_BYTES;    // the Q buffers between items: what the joins pass through
   // S buffers.  A third, where tensor memory has room for it, takes the scores of a block's next tile while the block's
-  // softmax still works on this one: chunks of D = 64 440 -> XXX us.
+  // softmax still works on this one: chunks of D = 64 beside decoding rows 441 -> 407 us.
   static constexpr int NBUF = D == 64 ? 3 : 2;
   static constexpr int N_BARS = 1 + 2 * NSK + 2 * NSV + 5 * NBUF + 2 + 1;
   static constexpr int SMEM = 1024 + NQ * Q_BYTES + (NSK + NSV) * KV_BYTES + 256 * 4 + N_BARS * 8 + 16;  // 256 floats: sM
@@ -936,28 +938,32 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
       const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
       p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
     };
-    // Which kernels run follows from the tokens a sequence has on average, since its length is on the device; any
-    // lengths run on either.  Rows of at most 32 per kv head: the kernel for few rows alone, 1.5 to 2.5 times as fast
-    // there (16 decoding tokens of 16000 keys: XXX against XXX us).  More: each sequence on the kernel that suits its
-    // own rows, if there may be sequences of both kinds (4 or more; decoding rows beside chunks: XXX -> XXX us,
-    // and 3 us for a launch that finds nothing).
+    // Which kernels run follows from the rows (tokens x heads of a kv head) that a sequence has on average, since its
+    // length is on the device; any lengths run on either.
+    // Up to one tile of the kernel for few rows (and the rows that a padded batch leaves free): that kernel alone.
+    // Measured, it against the other: 16 x 1 token of 16000 keys 85 against 112 us, 32 rows 219 against 249; 40 rows,
+    // its second tile reading the keys again, 393 against 259.
+    // More, in a batch of 16 or more, where there are likely to be sequences of both kinds: each on the kernel that
+    // suits its own rows (36 decoding beside 4 chunks 411 -> 403 us).  In a smaller one a launch that finds nothing
+    // costs more than that gives (4 chunks of 225 tokens 71 -> 77 us).
     const int64_t rows = plan->n_tokens * p.group;
-    const bool can_few = p.group <= kFewRows, few = can_few && rows <= (int64_t)40 * p.batch;
-    const bool both = !few && can_few && p.batch >= 4;
+    const bool can_few = p.group <= kFewRows, few = can_few && rows <= (int64_t)36 * p.batch;
+    const bool both = !few && can_few && p.batch >= 16;
     if (few || both) {
       if (both) p.rows_max = kFewRows;
       p.tb = kFewRows / p.group;
-      // Where a kv head's row does not fill the lines that L2 and HBM move, neighbouring heads share them, so the heads
-      // run side by side (CTA c takes head c % kvHeadNum) and find them in L2.  Below 140 busy SMs that would cost
-      // more than it gives.  Measured with 8 kv heads: rows of 160 bytes 690 -> 434 us, of 128 bytes 391 -> 353 us.
+      // The heads of a token lie side by side in the cache, so they run side by side, too: CTA c takes head c % kvHeadNum.
+      // DRAM pages are then read once, and rows that end inside a line find it in L2.  Below 140 busy SMs that would
+      // cost more than it gives.  Measured with 8 kv heads, rows of 160 bytes 690 -> 427 us, of 128 bytes 418 -> 330, of
+      // 256 bytes 626 -> 617, 32 query rows of them 219 -> 196.
       const int parts = kGrid / p.kv_heads;
-      p.head_stride = plan->row * 2 % 256 != 0 && parts * p.kv_heads >= 140 ? p.kv_heads : 1;
+      p.head_stride = parts * p.kv_heads >= 140 ? p.kv_heads : 1;
       set_small(128);
       e = launch_paged_few(plan->dtype, D, plan->tmK, plan->tmV, p, stream);
     }
     if (!few && e == cudaSuccess) {
-      // Two blocks of rows where sequences have more than one block's on average; at D = 64 there is room for both Q
-      // blocks and deep rings anyway.
+      // Two blocks of rows where sequences have more than one block's on average (256 rows: 218 us against 226 with one,
+      // long chunks 2290 against 2518); at D = 64 there is room for both Q blocks and deep rings anyway.
       const bool two = D == 64 || (D == 128 && rows > (int64_t)128 * p.batch);
       if (both) p.rows_min = kFewRows + 1;
       p.rows_max = INT32_MAX;

@@ -20,6 +20,10 @@ namespace {
 // few rows) and keeps them in shared memory; the CTAs then share the rows and the tokens.  The one order
 // between them, pushes before pops and reads of the inputs before writes of outputs that may be the same
 // memory, is a cluster barrier, so a step is one launch.
+//
+// Launch and a chain of memory latencies bound it.  Measured: 56 requests with one token each, one CTA: 6 us (2 of them
+// the launch).  1000 requests, 90 of them ended, 92000 tokens: 13.6 us with 16 CTAs (the largest cluster), 17 with 8,
+// 21 with one block move or token at a time.
 constexpr int kStepThreads = 1024;
 constexpr int kStepCluster = 16;
 
@@ -223,6 +227,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) paged_step_kernel(const Paged
 // Token t's K row goes to row slots[t] of the K cache and its V row to the same row of the V cache; slots
 // outside the cache (-1: padding) are skipped.  Nothing is computed: bytes bound it, so a thread has several
 // loads in flight before its first store.  `lanes` threads (a power of two) serve one token.
+// Measured: 40000 tokens of 8 heads of 128 in bf16: 51 to 53 us, 6.2 to 6.4 TB/s (a copy: 6.5); 120 tokens: 2 us, the launch.
 template <typename V>
 __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a, int lanes) {
   constexpr int U = 4;

@@ -7,19 +7,23 @@
 // A thread owns a key and half of the rows: it takes R / 2 scores, and its part of their sums stays in registers
 // until the item ends, so a tile needs no reduction at all.  The running maxima are common to all threads and only
 // move when some score is more than 2^8 above its row's (one vote of the threads a tile; under ALiBi too, since
-// tiles run from the last key to the first, the largest scores first).  P goes to shared memory as the products' second operand.
+// tiles run from the last key to the first, the largest scores first).  P goes to shared memory as the products'
+// second operand.
 // With R <= 16 the N columns are 2 R: the second R carry what rounding P to 16 bits dropped, which makes P V exact
 // to 2^-17 or so at no cost (N is at least 16, and the products are a tenth of the time).
 //
-// It is bound by the cache's bytes: 48 cycles of tensor work and some 500 of softmax a tile of 128 keys, against
-// 2700 (d = 128) that the tile takes to arrive at a CTA's share of HBM.  What is left for speed is to keep loads
-// in flight, so the rest of shared memory is one ring of K and V tiles in the order of their use (192 KB: 4.2 us
-// of HBM at a CTA's share), which also covers the change from one item to the next.
+// It is bound by the cache's bytes: some 500 cycles of tensor work and 1000 to 1700 of softmax a tile of 128 keys,
+// against 2700 (d = 128) that the tile takes to arrive at a CTA's share of HBM.  What is left for speed is to keep
+// loads in flight, so the rest of shared memory is one ring of K and V tiles in the order of their use (192 KB: 4.2 us
+// of HBM at a CTA's share), which also covers the change from one item to the next.  With pages of 16 rows, or row
+// tiles of 32 under ALiBi, issuing the boxes and the softmax take 1800 to 2000 cycles a tile and come to bound it.
+// Measured: 124 tokens over 9000 keys each, 32 / 8 heads, d 128: 617 us, 6.8 TB/s (a copy: 6.5 TB/s); one token over
+// 1000 keys: 9 us, the chain of its latencies.
 //
 // The line of tiles, its split over the CTAs and the partials of cut items are those of paged_attn.cu.
 //   warps 0..7  softmax (threads r and r + 128: key r of the tile, TMEM lane r, the first and the second half of
 //               the rows) and epilogue (column r of O)
-//   warp 8      TMA producer;  warp 9  tcgen05 issuer
+//   warps 8, 9  TMA producers of K and of V;  warp 10  tcgen05 issuer
 #include "paged_common.cuh"
 
 namespace ala {
@@ -31,7 +35,9 @@ struct Few {
   static constexpr int D = D_, TK = 128, CB = D / 64;
   static constexpr int KV_BYTES = TK * D * 2;
   static constexpr int NS = 192 * 1024 / KV_BYTES;  // ring slots
-  static constexpr int MT = D == 256 ? 2 : 1;       // 128-row tiles of O^T (D = 64: its upper lanes are not read)
+  // 128-row tiles of O^T.  With D = 64 the lanes from 64 on multiply what lies behind a V tile, in shared memory still,
+  // and are read by nobody.
+  static constexpr int MT = D == 256 ? 2 : 1;
   static constexpr int QCB = kFewRows * 128;        // bytes of a 64-column block of Q
   static constexpr int Q_BYTES = CB * QCB;
   static constexpr int P_BYTES = 2 * QCB;           // [2 blocks of 64 keys][32 rows][128 B]
@@ -39,6 +45,7 @@ struct Few {
   static constexpr int THREADS = 352;
   static constexpr int SMEM = 1024 + NS * KV_BYTES + Q_BYTES + 2 * P_BYTES + N_BARS * 8 + 16;
   static constexpr uint32_t O_COL = 64, TMEM_COLS = 128;  // S^T [0, 32) and [32, 64), O^T from 64
+  static_assert(D != 64 || Q_BYTES + 2 * P_BYTES >= KV_BYTES, "behind the last V tile");
   static_assert(SMEM + 1400 <= 232448, "shared memory budget (1400: the static part)");
 };
 

@@ -9,8 +9,9 @@
 // move when some score is more than 2^8 above its row's (one vote of the threads a tile; under ALiBi too, since
 // tiles run from the last key to the first, the largest scores first).  P goes to shared memory as the products'
 // second operand.
-// With R <= 16 the N columns are 2 R: the second R carry what rounding P to 16 bits dropped, which makes P V exact
-// to 2^-17 or so at no cost (N is at least 16, and the products are a tenth of the time).
+// With R <= 16, and in the difference of two maps, the N columns are 2 R: the second R carry what rounding P to 16
+// bits dropped, which makes P V exact to 2^-17 or so at no cost (N is at least 16, and the products are a tenth of
+// the time).
 //
 // It is bound by the cache's bytes: some 500 cycles of tensor work and 1000 to 1700 of softmax a tile of 128 keys,
 // against 2700 (d = 128) that the tile takes to arrive at a CTA's share of HBM.  What is left for speed is to keep
@@ -44,7 +45,7 @@ struct Few {
   static constexpr int N_BARS = 1 + 2 * NS + 6 + 2;
   static constexpr int THREADS = 352;
   static constexpr int SMEM = 1024 + NS * KV_BYTES + Q_BYTES + 2 * P_BYTES + N_BARS * 8 + 16;
-  static constexpr uint32_t O_COL = 64, TMEM_COLS = 128;  // S^T [0, 32) and [32, 64), O^T from 64
+  static constexpr uint32_t O_COL = 64, TMEM_COLS = 256;  // S^T [0, 32) and [32, 64), O^T from 64, 64 columns a tile
   static_assert(D != 64 || Q_BYTES + 2 * P_BYTES >= KV_BYTES, "behind the last V tile");
   static_assert(SMEM + 1400 <= 232448, "shared memory budget (1400: the static part)");
 };
@@ -108,18 +109,21 @@ struct FewState {
 
 // One item: its key tiles and its epilogue, R rows, RT of them this thread's.  After a failed wait a warp skips the waits that are left, but
 // goes through every tile and item, so that the warps meet as often as ever.
-template <typename T, int D, int R>
+template <typename T, int D, int R, int MAPS>
 __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>& w, FewState& f, RowTables& tab, uint8_t* sVring,
                                          uint32_t v_slot0, uint64_t* v_full0, uint32_t v_phase0, uint32_t sP, uint64_t* s_full,
                                          uint64_t* p_full, uint64_t* pv_done, uint64_t* o_done, uint32_t tmem, int64_t token0,
                                          int tokens) {
   using C = Few<T, D>;
-  constexpr bool kCarry = R <= 16;
+  constexpr bool kCarry = R <= 16 || MAPS == 2;
+  // 32 rows and what their rounding drops: P takes both buffers, [2 blocks of 64 keys][64 rows][128 B]
+  constexpr bool kOneP = R == 32 && kCarry;
+  constexpr int PCB = kOneP ? 2 * C::QCB : C::QCB;
   constexpr int RT = R / 2;
   const int r = threadIdx.x & 127, quarter = r >> 5, lane = r & 31;
   const int n0 = (threadIdx.x >> 7) * RT;  // this thread's rows: n0 .. n0 + RT - 1
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  const int group = p.group, rows = tokens * group, mt = p.mask_type, maps = p.maps();
+  const int group = p.group, rows = tokens * group, mt = p.mask_type;
   const bool alibi = mt == 3 || mt == 4 || mt == 5;
   const float scale = p.scale_log2;
   int* status = p.status;
@@ -133,7 +137,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
     l[n] = 0.f;
   }
   // this key's place in a row of P: [block of 64 keys][row][128 B], 16-byte chunks swizzled by the row
-  const uint32_t pk0 = (r >> 6) * C::QCB + (r & 7) * 2, pchunk = (r & 63) >> 3;
+  const uint32_t pk0 = (r >> 6) * PCB + (r & 7) * 2, pchunk = (r & 63) >> 3;
   const int cnt = w.t1 - w.t0;
   for (int u = 0; u < cnt; ++u, ++f.g) {
     const int j0 = (w.t1 - 1 - u) * 128, key = j0 + r;
@@ -188,7 +192,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
         for (int mi = 0; mi < C::MT; ++mi)
 #pragma unroll
           for (int part = 0; part < (kCarry ? 2 : 1); ++part) {
-            const uint32_t col = tmem + lanes + C::O_COL + mi * 32 + part * R + n0;
+            const uint32_t col = tmem + lanes + C::O_COL + mi * 64 + part * R + n0;
             uint32_t o[RT];
             ld_cols<RT>(col, o);
             tmem_ld_wait();
@@ -214,9 +218,11 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
       }
     }
     // the buffer's previous P has been multiplied
-    if (u >= 2 && f.ok)
-      f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + b, ((f.g >> 1) - 1) & 1, status, kDevTimeoutODone));
-    const uint32_t prow = sP + b * C::P_BYTES + pk0 + n0 * 128;
+    if (u >= (kOneP ? 1 : 2) && f.ok) {
+      const uint32_t before = f.g - (kOneP ? 1 : 2);
+      f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (before & 1), (before >> 1) & 1, status, kDevTimeoutODone));
+    }
+    const uint32_t prow = sP + (kOneP ? 0 : b * C::P_BYTES) + pk0 + n0 * 128;
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
       const uint32_t at = prow + n * 128 + ((pchunk ^ ((n0 + n) & 7)) << 4);
@@ -274,7 +280,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
 #pragma unroll
   for (int mi = 0; mi < C::MT; ++mi) {
     uint32_t raw[RT], rest[RT];
-    const uint32_t col = tmem + lanes + C::O_COL + mi * 32 + n0;
+    const uint32_t col = tmem + lanes + C::O_COL + mi * 64 + n0;
     ld_cols<RT>(col, raw);
     if constexpr (kCarry) ld_cols<RT>(col + R, rest);
     tmem_ld_wait();
@@ -294,7 +300,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
       for (int n = 0; n < RT; ++n)
         if (n0 + n < rows) dst[(int64_t)n * D] = o[mi][n];
     }
-  } else if (maps == 1) {
+  } else if constexpr (MAPS == 1) {
     // the rows of one token follow each other; the next token's lie p.heads rows on
     int hh = n0 % group;
     T* dst = static_cast<T*>(p.out) + ((token0 + n0 / group) * p.heads + w.h * group + hh) * p.row + r;
@@ -363,7 +369,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int MAPS>
 __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PagedParams p) {
@@ -510,7 +516,9 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       const int cnt = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       const int rows = __shfl_sync(0xffffffffu, w.tokens(p) * p.group, 0);
       const uint32_t idesc_qk = instr_desc(ElemFmt<T>::fmt, false, false, 128, rows <= 16 ? 16 : 32);
-      const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, true, false, 128, rows <= 8 ? 16 : 32);
+      const bool one_p = MAPS == 2 && rows > 16;  // few_item's kOneP
+      const uint32_t idesc_pv = instr_desc(ElemFmt<T>::fmt, true, false, 128, rows <= 8 ? 16 : one_p ? 64 : 32);
+      const uint32_t p_cb = (one_p ? 2 * C::QCB : C::QCB) >> 4;
       auto issue_qk = [&](uint32_t b) -> bool {
         if (!wait_all(full + slot, phase, kDevTimeoutKFull)) return false;
         tc_fence_after();
@@ -533,13 +541,13 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         ok = wait_warp2(full + slot, phase, kDevTimeoutVFull, p_full + b, (g >> 1) & 1, kDevTimeoutPFull, status);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a0 = dv + slot * kStep, b0 = dp + b * kPStep;
+        const uint64_t a0 = dv + slot * kStep, b0 = dp + (one_p ? 0 : b * kPStep);
 #pragma unroll
         for (int mi = 0; mi < C::MT; ++mi)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss_by(lead, tmem + C::O_COL + mi * 32, a0 + mi * ((2 * 128 * 128) >> 4) + kk * ((16 * 128) >> 4),
-                      b0 + (kk / 4) * (C::QCB >> 4) + (kk % 4) * 2, idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
+            mma_ss_by(lead, tmem + C::O_COL + mi * 64, a0 + mi * ((2 * 128 * 128) >> 4) + kk * ((16 * 128) >> 4),
+                      b0 + (kk / 4) * p_cb + (kk % 4) * 2, idesc_pv, (u > 0 || kk > 0) ? 1u : 0u);
         mma_commit_by(lead, empty + slot);
         mma_commit_by(lead, pv_done + b);
         if (u == cnt - 1) mma_commit_by(lead, o_done);
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   } else {
     // -------------------------------------------------------------- softmax and epilogue
     const int r = threadIdx.x;
-    const int group = p.group, maps = p.maps();
+    const int group = p.group;
     FewState f{0, 0, true};
     uint32_t loads = 0;  // ring slots used so far
     if (r == 0) tab.join[0].n_seg = tab.join[1].n_seg = 0;
@@ -575,7 +583,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       for (int i = r; i < R * (D / 8); i += 256) {
         const int row = i / (D / 8), c = i % (D / 8);
         const int qh = w.h * group + row % group;
-        const int lo = maps == 2 ? (qh & 1) * (p.dq / 8) : 0;  // map 2 in the upper half
+        const int lo = MAPS == 2 ? (qh & 1) * (p.dq / 8) : 0;  // map 2 in the upper half
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < rows && c >= lo && c < lo + p.dq / 8)
           v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (token0 + row / group) * p.q_stride + (int64_t)qh * p.dq) + (c - lo));
@@ -591,11 +599,11 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
       const uint32_t v_phase0 = (v0 / NS) & 1;
       const uint32_t sp = smem_addr(sP);
       if (R == 8)
-        few_item<T, D, 8>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+        few_item<T, D, 8, MAPS>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
       else if (R == 16)
-        few_item<T, D, 16>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+        few_item<T, D, 16, MAPS>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
       else
-        few_item<T, D, 32>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
+        few_item<T, D, 32, MAPS>(p, w, f, tab, ring, v0 % NS, v_full0, v_phase0, sp, s_full, p_full, pv_done, o_done, tmem, token0, tokens);
       loads += 2 * cnt;
       if (w.t0 > 0 || w.t1 < w.n) {
         // ---- a cut item: whoever brings its last segment joins them, so nobody waits
@@ -620,10 +628,10 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
     // ---- the joins that fell to this CTA, both items' rows side by side (after the loop, so that what a join holds in
     // registers does not weigh on the tiles)
     named_barrier_sync(1, 256);
-    const int n0 = tab.join[0].n_seg ? tab.join[0].tokens * group / maps : 0, n1 = tab.join[1].n_seg ? tab.join[1].tokens * group / maps : 0;
+    const int n0 = tab.join[0].n_seg ? tab.join[0].tokens * group / MAPS : 0, n1 = tab.join[1].n_seg ? tab.join[1].tokens * group / MAPS : 0;
     for (int o = warp; o < n0 + n1; o += 8) {
-      const int k = o < n0 ? 0 : 1, row = o - k * n0, gh = group / maps;
-      combine_row<T, D>(p, tab.join[k], tab.first[k], row / gh, row % gh);
+      const int k = o < n0 ? 0 : 1, row = o - k * n0, gh = group / MAPS;
+      combine_row<T, D, MAPS>(p, tab.join[k], tab.first[k], row / gh, row % gh);
     }
   }
 
@@ -636,12 +644,17 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   }
 }
 
+template <typename T, int D, int MAPS>
+cudaError_t launch_maps(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, cudaStream_t stream) {
+  using C = Few<T, D>;
+  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<T, D, MAPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_few_kernel<T, D, MAPS>, dim3(kGrid), C::THREADS, C::SMEM, stream, tmK, tmV, p);
+}
+
 template <typename T, int D>
 cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p, cudaStream_t stream) {
-  using C = Few<T, D>;
-  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(paged_few_kernel<T, D>, dim3(kGrid), C::THREADS, C::SMEM, stream, tmK, tmV, p);
+  return p.maps() == 1 ? launch_maps<T, D, 1>(tmK, tmV, p, stream) : launch_maps<T, D, 2>(tmK, tmV, p, stream);
 }
 
 }  // namespace

@@ -204,6 +204,34 @@ def test_differential_groups(heads, kv_heads, mask):
     _check(paged_ref.make_case(lens, heads, kv_heads, 64, BF, 16, mask, 800 + heads, maps=2, norm=heads % 2 == 0))
 
 
+@pytest.mark.parametrize("d", [16, 24, 32, 64, 128])
+@pytest.mark.parametrize("heads,kv_heads,new", [(2, 1, 1), (8, 1, 1), (12, 1, 1), (16, 1, 1), (6, 3, 2), (8, 2, 4), (4, 4, 9)])
+def test_differential_few_rows(heads, kv_heads, new, d):
+    # 4 to 32 rows of a kv head, whole items and cut ones, the norm and none
+    lens = [(new, 2000), (1, 150), (new, 333), (0, 9), (new, max(new, 5))]
+    _check(paged_ref.make_case(lens, heads, kv_heads, d, FP if d == 32 else BF, 32, 9, 850 + d + heads, maps=2, norm=d != 64, tail=2))
+
+
+@pytest.mark.parametrize("mask", [0, 3, 4, 5, 9])
+@pytest.mark.parametrize("heads,kv_heads,new,d", [(2, 2, 1, 64), (16, 1, 1, 128), (32, 1, 1, 64), (10, 2, 5, 80), (4, 1, 8, 128), (6, 2, 3, 40)])
+def test_few_rows(heads, kv_heads, new, d, mask):
+    lens = [(new, 2000), (1, 150), (new, 333), (0, 9), (new, max(new, 5))]
+    _check(paged_ref.make_case(lens, heads, kv_heads, d, FP if d == 80 else BF, 32, mask, 870 + d + heads, tail=2))
+
+
+@pytest.mark.parametrize("d", [136, 192, 256])
+def test_few_rows_of_large_heads(d):
+    for heads, kv_heads, new in ((4, 2, 1), (16, 1, 1), (8, 1, 4)):
+        _check(paged_ref.make_case([(new, 1500), (new, 70), (1, 300)], heads, kv_heads, d, BF, 64, 9, 890 + d, tail=1))
+
+
+def test_few_rows_in_a_batch_too_large_for_one_scan():
+    # more than 64 sequences, more than the threads of a CTA, single tokens: every CTA scans the batch in steps
+    rng = random.Random(9)
+    lens = [(1, rng.choice([1, 2, 40, 129, 300])) for _ in range(700)] + [(0, 5)] * 3
+    _check(paged_ref.make_case(lens, 4, 2, 64, BF, 16, 9, 895))
+
+
 def test_one_plan_serves_changing_lengths_and_a_captured_graph():
     c = paged_ref.make_case([(1, 900), (2, 500), (1, 40), (60, 300)], 8, 2, 64, BF, 16, 9, 900, tail=10)
     op, out, lse = _plan(c)

@@ -409,12 +409,14 @@ ALA_API int ala_paged_write(const ala_tensor* key, int64_t keyStride, const ala_
  *
  * A row without a key (kvSeqLen 0, or kvSeqLen < seqLen) gets output 0 and
  * lse -inf.  Slots past kvSeqLen may hold anything, NaN included; rows within
- * kvSeqLen must be finite.
+ * kvSeqLen must be finite.  A query row with a NaN makes its own output and
+ * lse NaN and no other.
  * Lengths are checked on the device: a negative one counts as 0, new tokens
  * past nTokens are dropped, keys past maxBlockNum blocks too, and
- * ala_workspace_status then reports 0x10C; a block-table entry in use outside
- * [0, numBlocks) reads as zeros and reports 0x10B.  Both leave later
- * executions unaffected.
+ * ala_workspace_status then reports 0x10C; what the rows of such a sequence
+ * hold is unspecified, the others' are right.  A block-table entry in use
+ * outside [0, numBlocks) reads as zeros and reports 0x10B.  Both leave the
+ * outputs of later executions unaffected.
  * Results do not depend on which execution or graph replay computes them
  * (no atomics in sums), but may differ in rounding with the other sequences
  * of the batch, which decide where a long row is split.

@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
             __syncwarp();
           }
           if (valid && p.lse) {
-            float lse = rs.l > 0.f ? rs.m * kLn2 + logf(rs.l) : -INFINITY;
+            float lse = rs.l != 0.f ? rs.m * kLn2 + logf(rs.l) : -INFINITY;
             if (p.mask_type == 5) lse += p.slopes[qh] * static_cast<float>(rs.pos);  // left-aligned = right-aligned + slope * pos
             p.lse[token * p.heads + qh] = lse;
           }

@@ -549,7 +549,7 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);
   } else if (p.lse && lane == 0) {
-    float lse = sum[0] > 0.f ? top[0] * kLn2 + logf(sum[0]) : -INFINITY;
+    float lse = sum[0] != 0.f ? top[0] * kLn2 + logf(sum[0]) : -INFINITY;
     if (p.mask_type == 5) lse += p.slopes[head] * static_cast<float>(d.pos0 + tok);
     p.lse[(int64_t)token * p.heads + head] = lse;
   }

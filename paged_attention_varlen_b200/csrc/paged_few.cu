@@ -271,7 +271,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
       p.ml[prow0 + n] = make_float2(top, sum);
     } else if (p.lse) {
       const int h = w.h * group + n % group;
-      float lse = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+      float lse = sum != 0.f ? top * kLn2 + logf(sum) : -INFINITY;
       if (mt == 5) lse += p.slopes[h] * static_cast<float>(tab.pos[n]);  // left-aligned = right-aligned + slope * position
       p.lse[(token0 + n / group) * p.heads + h] = lse;
     }

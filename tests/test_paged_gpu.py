@@ -161,6 +161,31 @@ def test_rows_without_a_key():
     assert (out[:4] == 0).all()
 
 
+@pytest.mark.parametrize("lens", [[(1, 40), (1, 5000), (2, 300)], [(140, 900), (3, 20)], [(200, 30000)]])
+@pytest.mark.parametrize("maps,d", [(1, 64), (1, 128), (1, 256), (2, 32), (2, 64), (2, 128)])
+def test_a_query_with_a_nan_spoils_its_own_row_only(maps, d, lens):
+    c = paged_ref.make_case(lens, 4, 2, d, BF, 16, 9, 655 + d, maps=maps)
+    q, n = c["q"].cuda(), c["q"].shape[0]
+    bad = [(0, 1), (n - 1, 2), (n // 2, 3)]  # (token, head), of one map
+    for t, h in bad:
+        q[t, maps * h, 5] = float("nan")
+    op, out, lse = _plan(c, q=q)
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    ref, lref, tol, ltol = paged_ref.attention(c)
+    good = torch.ones(n, 4, dtype=torch.bool)
+    for t, h in bad:
+        good[t, h] = False
+    got = out.cpu().double()
+    assert got[~good].isnan().all()
+    assert ((got[good] - ref[good]).abs() <= tol[good]).all()
+    if lse is not None:
+        l = lse.cpu().double()
+        assert l[~good].isnan().all()
+        assert ((l[good] - lref[good]).abs() <= ltol[good]).all()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 def test_scales(scale):
     c = paged_ref.make_case([(1, 200), (40, 90)], 4, 2, 64, FP, 16, 9, 660)

@@ -52,7 +52,7 @@ struct Few {
 
 // What the threads share about an item's rows, and the scratch of their reductions.
 struct RowTables {
-  float slope_log2[kFewRows];  // of the row's head
+  float4 bias[kFewRows / 2];   // of rows 2i and 2i + 1: slopes of their heads (log2 units), minus their tokens' places in the tile
   int pos[kFewRows];           // position of the row's token
   int last_key[kFewRows];      // keys up to this one are allowed (-1: none)
   float m[kFewRows];
@@ -128,6 +128,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
   const float scale = p.scale_log2;
   int* status = p.status;
   const int first_last = tab.last_key[0];  // the earliest token sees fewest keys
+  const int pos0 = tab.pos[0];
   // Maxima in log2 units (the ones P is computed against) and sums.  A row that has met no key has a maximum below
   // any score, and finite, so that it needs no case of its own.
   float m[RT], l[RT];
@@ -151,11 +152,21 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
 #pragma unroll
     for (int n = 0; n < RT; ++n) t[n] = __uint_as_float(raw[n]) * scale;
     if (alibi) {
+      // right- and left-aligned bias differ by a per-row constant; both use (key - pos), which is exact below 2^24 as a
+      // difference of 32-bit floats too: one conversion a thread, pairs of rows in one instruction
+      const float ahead0 = static_cast<float>(key - pos0);
 #pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        // right- and left-aligned bias differ by a per-row constant; both use (key - pos)
-        const float ahead = static_cast<float>(key - tab.pos[n0 + n]), s = tab.slope_log2[n0 + n];
-        t[n] = mt == 4 ? fmaf(-s, sqrt_approx(fmaxf(-ahead, 0.f)), t[n]) : fmaf(s, ahead, t[n]);
+      for (int n = 0; n < RT; n += 2) {
+        const float4 sb = tab.bias[(n0 + n) / 2];
+        const uint64_t ahead = add_x2(f2pack(ahead0, ahead0), f2pack(sb.z, sb.w));
+        if (mt == 4) {
+          float a0, a1;
+          f2unpack(ahead, a0, a1);
+          t[n] = fmaf(-sb.x, sqrt_approx(fmaxf(-a0, 0.f)), t[n]);
+          t[n + 1] = fmaf(-sb.y, sqrt_approx(fmaxf(-a1, 0.f)), t[n + 1]);
+        } else {
+          f2unpack(fma_x2(f2pack(sb.x, sb.y), ahead, f2pack(t[n], t[n + 1])), t[n], t[n + 1]);
+        }
       }
     }
     if (j0 + 127 > first_last) {
@@ -577,7 +588,9 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         tab.pos[r] = pos;
         // rows that fill up R see every key, so that they never decide whether a tile needs masks
         tab.last_key[r] = p.mask_type == 0 || r >= rows ? w.s.kv - 1 : min(pos, w.s.kv - 1);
-        tab.slope_log2[r] = p.slopes && r < rows ? p.slopes[w.h * group + r % group] * kLog2e : 0.f;
+        float* bias = reinterpret_cast<float*>(&tab.bias[r / 2]) + (r & 1);
+        bias[0] = p.slopes && r < rows ? p.slopes[w.h * group + r % group] * kLog2e : 0.f;
+        bias[2] = -static_cast<float>(r / group);
       }
       // ---- Q, K-major with the 128-byte swizzle, zeros in the rows that fill up R and behind the row's columns
       for (int i = r; i < R * (D / 8); i += 256) {

@@ -228,11 +228,10 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
         lo[n / 2] = pack2(e0 - h.x, e1 - h.y, (T*)nullptr);
       }
     }
-    // the buffer's previous P has been multiplied
-    if (u >= (kOneP ? 1 : 2) && f.ok) {
-      const uint32_t before = f.g - (kOneP ? 1 : 2);
-      f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (before & 1), (before >> 1) & 1, status, kDevTimeoutODone));
-    }
+    // The buffer's previous P has been multiplied: two tiles back that product was issued before this tile's scores,
+    // and a commit waits for all products before it.
+    if (kOneP && u > 0 && f.ok)
+      f.ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (b ^ 1), ((f.g - 1) >> 1) & 1, status, kDevTimeoutODone));
     const uint32_t prow = sP + (kOneP ? 0 : b * C::P_BYTES) + pk0 + n0 * 128;
 #pragma unroll
     for (int n = 0; n < RT; ++n) {

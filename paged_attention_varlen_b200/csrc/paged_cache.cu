@@ -284,7 +284,10 @@ cudaError_t write_as(const PagedWriteArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_paged_step(const PagedStepArgs& a, cudaStream_t stream) {
   const int smem = (int)sizeof(StepRow) * (a.batch + 1);
-  const bool small = a.n_tokens <= 1024 && a.batch <= 256;
+  // One CTA of 256 threads where that has little to do, else the cluster, whose barrier and wider sums cost 1 us.  One CTA
+  // against the cluster, 1000 keys each: 1 request 3.1 and 4.3 us, 56 5.6 and 6.1, 128 7.3 and 6.1, 256 10.2 and 6.2; 4 of
+  // 256 tokens 4.5 and 5.6, 8 of 256 6.4 and 5.8.
+  const bool small = a.n_tokens <= 1024 && a.batch <= 64;
   if (!small) {
     const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

@@ -412,6 +412,21 @@ def test_step(batch, width, block, in_place):
         assert tables == wtables and free == wfree
 
 
+@pytest.mark.parametrize("batch", [63, 64, 65])
+@pytest.mark.parametrize("tokens", [1000, 1024, 1025, 1500])
+def test_step_with_one_block_of_threads_and_with_many(batch, tokens):
+    rng = random.Random(batch * tokens)
+    seq, *rest, n_tokens = _step_case(rng, batch, 40, 16)
+    assert sum(seq) <= n_tokens
+    n_tokens = max(tokens, sum(seq))
+    want = paged_ref.step(seq, *rest, n_tokens)
+    out, tables, free = _run_step(seq, *rest, n_tokens)
+    assert out.status.item() == 0
+    got = [out.kv_seq_len.tolist(), out.free_count.item(), out.cu_seq_len.tolist(), out.slot_mapping.tolist(),
+           out.positions.tolist(), tables, free]
+    assert got == list(want)
+
+
 def test_step_that_cannot_be_served_changes_nothing():
     rng = random.Random(1)
     for batch in (5, 1500):

@@ -363,7 +363,7 @@ def _same_device(first, **tensors):
 
 
 def _index(device) -> int:
-    """CUDA ordinal of ``device``; -1 for a device that nothing can be launched on."""
+    """CUDA ordinal of ``device``; -1 for a device that nothing can be launched on (_launch refuses it)."""
     if device.type != "cuda":
         return -1
     return device.index if device.index is not None else torch.cuda.current_device()
@@ -371,6 +371,8 @@ def _index(device) -> int:
 
 def _launch(index, stream, function, args):
     """function(*args, stream handle) with device ``index`` current; raises the library's error."""
+    if index < 0:  # the kernels would follow host pointers: the C ABI cannot tell, and device -1 means "the current one"
+        raise ValueError("the tensors of this call are not on a CUDA device")
     # the raw handle of the current stream: torch.cuda.current_stream builds a Stream object first, which costs a
     # small call as much as its launch
     s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
@@ -400,7 +402,7 @@ class PagedOp(Op):
         self._args = (self.workspace.data_ptr(), self.workspace_size, self._handle)
 
     def __call__(self, stream: torch.cuda.Stream | None = None):
-        if not self._bound and not _capturing(stream):
+        if not self._bound and (self._index < 0 or not _capturing(stream)):
             _launch(self._index, stream, lib().ala_op_bind_workspace,
                     (self._handle, self.workspace.data_ptr(), self.workspace_size))
             self._bound = True

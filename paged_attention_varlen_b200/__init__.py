@@ -394,7 +394,9 @@ def _capturing(stream) -> bool:
 
 class PagedOp(Op):
     """A planned paged attention call.  Its first execution binds the workspace (a synchronisation), unless the
-    stream is being captured; a captured execution needs no binding."""
+    stream is being captured; a captured execution needs no binding.  A nonzero status stays in a bound workspace:
+    after ``device_status`` has returned one, the next call, what is captured from then on, or ``bind()`` clears it
+    (a loop that only replays a graph captured before has to ``bind()``)."""
 
     def __init__(self, handle, ws_size, execute_fn, device, keep):
         super().__init__(handle, ws_size, execute_fn, device, keep)
@@ -403,11 +405,25 @@ class PagedOp(Op):
 
     def __call__(self, stream: torch.cuda.Stream | None = None):
         if not self._bound and (self._index < 0 or not _capturing(stream)):
-            _launch(self._index, stream, lib().ala_op_bind_workspace,
-                    (self._handle, self.workspace.data_ptr(), self.workspace_size))
-            self._bound = True
+            self.bind(stream)
         _launch(self._index, stream, self._execute, self._args)
         return self
+
+    def bind(self, stream: torch.cuda.Stream | None = None):
+        """Clear the workspace's status words and what a wait that ran out left behind, without an execution.  Waits for
+        ``stream``, which has to come after every execution and may not be capturing."""
+        if self._index >= 0 and _capturing(stream):
+            raise RuntimeError("a workspace cannot be bound while its stream is being captured")
+        _launch(self._index, stream, lib().ala_op_bind_workspace,
+                (self._handle, self.workspace.data_ptr(), self.workspace_size))
+        self._bound = True
+        return self
+
+    def device_status(self) -> int:
+        code = super().device_status()
+        if code != 0:  # unbound on the library's side too, so that a captured execution holds the clear of the status words
+            _check(lib().ala_op_bind_workspace(self._handle, None, 0, None))
+        return code
 
 
 class PagedCall:

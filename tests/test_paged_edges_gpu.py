@@ -1,0 +1,81 @@
+"""Edges of the paged serving operators on the GPU."""
+import pytest
+import torch
+
+import paged_attention_varlen_b200 as ala
+import paged_ref
+from test_paged_gpu import BF, _compare, _plan
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from paged_attention_varlen_b200 import build
+    build.build()
+
+
+def _graph(op):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op()
+    return graph
+
+
+# ---------------------------------------------------------------------------------------------- status
+
+@pytest.mark.parametrize("lens", [[(1, 200), (1, 90)], [(60, 200), (40, 90)]])
+def test_a_status_that_was_read_is_gone_from_what_is_captured_after_it(lens):
+    c = paged_ref.make_case(lens, 4, 2, 64, BF, 16, 9, 10)
+    op, out, lse = _plan(c)
+    tables = op._keep[3]
+    tables[0, 3] = -1
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0x10B
+    tables.copy_(c["tables"])
+    graph = _graph(op)
+    for _ in range(2):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert op.device_status() == 0
+        _compare(c, out, lse)
+
+
+@pytest.mark.parametrize("lens", [[(1, 200), (1, 90)], [(60, 200), (40, 90)]])
+def test_binding_clears_the_status_of_a_loop_of_replays(lens):
+    c = paged_ref.make_case(lens, 4, 2, 64, BF, 16, 9, 20)
+    op, out, lse = _plan(c)
+    op()
+    graph = _graph(op)
+    tables = op._keep[3]
+    tables[0, 3] = -1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0x10B
+    tables.copy_(c["tables"])
+    op.bind()
+    out.fill_(7.0)
+    lse.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    _compare(c, out, lse)
+
+
+def test_binding_is_refused_on_a_stream_that_is_captured():
+    c = paged_ref.make_case([(1, 40)], 4, 2, 64, BF, 16, 9, 25)
+    op, out, lse = _plan(c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError):
+            op.bind()
+        op()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    _compare(c, out, lse)

@@ -916,6 +916,12 @@ void paged_layout(PagedPlan* plan) {
 }
 
 int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, size_t errlen) {
+  cudaError_t e = cudaSuccess;
+  if (workspace != plan->bound_ws) e = cudaMemsetAsync(workspace, 0, kPagedHeaderBytes, stream);
+  if (e != cudaSuccess) {
+    snprintf(err, errlen, "status clear failed: %s", cudaGetErrorString(e));
+    return ALA_CUDA_ERROR;
+  }
   if (plan->n_tokens == 0 || plan->batch == 0) return ALA_OK;  // no rows to write
   const int D = paged_kernel_d(plan->row);
   const int box = kv_box_rows(plan->block_size, D == 256 ? 64 : 128);
@@ -932,81 +938,77 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     plan->maps_ready = true;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  cudaError_t e = cudaSuccess;
-  if (workspace != plan->bound_ws) e = cudaMemsetAsync(workspace, 0, kPagedHeaderBytes, stream);
-  if (e == cudaSuccess) {
-    PagedParams p{};
-    p.seq_len = plan->seq_len;
-    p.kv_seq_len = plan->kv_seq_len;
-    p.block_tables = plan->block_tables;
-    p.slopes = plan->slopes;
-    p.lambda = plan->lambda;
-    p.norm_weight = plan->norm_weight;
-    p.q = plan->q;
-    p.out = plan->out;
-    p.lse = plan->lse;
-    p.status = reinterpret_cast<int*>(ws);
-    p.arrived = reinterpret_cast<int*>(ws + 256);
-    p.desc = reinterpret_cast<PagedDesc*>(ws + plan->off_desc);
-    p.ml = reinterpret_cast<float2*>(ws + plan->off_ml);
-    p.part = reinterpret_cast<float*>(ws + plan->off_part);
-    p.q_stride = plan->q_stride;
-    p.n_tokens = (int32_t)plan->n_tokens;
-    p.batch = plan->batch;
-    p.max_blocks = plan->max_blocks;
-    p.block_size = plan->block_size;
-    p.num_blocks = plan->num_blocks;
-    p.mask_type = plan->mask_type;
-    p.heads = plan->heads;
-    p.kv_heads = plan->kv_heads;
-    p.group = plan->heads / plan->kv_heads;
-    p.dq = plan->d;
-    p.row = plan->row;
-    p.tb1 = 128 / p.group;
-    p.scale_log2 = plan->qk_scale * kLog2e;
-    p.norm_eps = plan->norm_eps;
-    p.out_scale = plan->out_scale;
-    p.box_rows = box;
-    p.rows_min = 0;
+  PagedParams p{};
+  p.seq_len = plan->seq_len;
+  p.kv_seq_len = plan->kv_seq_len;
+  p.block_tables = plan->block_tables;
+  p.slopes = plan->slopes;
+  p.lambda = plan->lambda;
+  p.norm_weight = plan->norm_weight;
+  p.q = plan->q;
+  p.out = plan->out;
+  p.lse = plan->lse;
+  p.status = reinterpret_cast<int*>(ws);
+  p.arrived = reinterpret_cast<int*>(ws + 256);
+  p.desc = reinterpret_cast<PagedDesc*>(ws + plan->off_desc);
+  p.ml = reinterpret_cast<float2*>(ws + plan->off_ml);
+  p.part = reinterpret_cast<float*>(ws + plan->off_part);
+  p.q_stride = plan->q_stride;
+  p.n_tokens = (int32_t)plan->n_tokens;
+  p.batch = plan->batch;
+  p.max_blocks = plan->max_blocks;
+  p.block_size = plan->block_size;
+  p.num_blocks = plan->num_blocks;
+  p.mask_type = plan->mask_type;
+  p.heads = plan->heads;
+  p.kv_heads = plan->kv_heads;
+  p.group = plan->heads / plan->kv_heads;
+  p.dq = plan->d;
+  p.row = plan->row;
+  p.tb1 = 128 / p.group;
+  p.scale_log2 = plan->qk_scale * kLog2e;
+  p.norm_eps = plan->norm_eps;
+  p.out_scale = plan->out_scale;
+  p.box_rows = box;
+  p.rows_min = 0;
+  p.rows_max = INT32_MAX;
+  auto set_small = [&](int tk) {
+    const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
+    p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
+  };
+  // Which kernels run follows from the rows (tokens x heads of a kv head) that a sequence has on average, since its
+  // length is on the device; any lengths run on either.
+  // Up to one tile of the kernel for few rows (and the rows that a padded batch leaves free): that kernel alone.
+  // Measured, it against the other: 16 x 1 token of 16000 keys 85 against 112 us, 32 rows 219 against 249; 40 rows,
+  // its second tile reading the keys again, 393 against 259.
+  // More, in a batch of 16 or more, where there are likely to be sequences of both kinds: each on the kernel that
+  // suits its own rows (36 decoding beside 4 chunks 411 -> 403 us).  In a smaller one a launch that finds nothing
+  // costs more than that gives (4 chunks of 225 tokens 71 -> 77 us).
+  const int64_t rows = plan->n_tokens * p.group;
+  const bool can_few = p.group <= kFewRows, few = can_few && rows <= (int64_t)36 * p.batch;
+  const bool both = !few && can_few && p.batch >= 16;
+  if (few || both) {
+    if (both) p.rows_max = kFewRows;
+    p.tb = kFewRows / p.group;
+    // The heads of a token lie side by side in the cache, so they run side by side, too: CTA c takes head c % kvHeadNum.
+    // DRAM pages are then read once, and rows that end inside a line find it in L2.  Below 140 busy SMs that would
+    // cost more than it gives.  Measured with 8 kv heads, rows of 160 bytes 690 -> 427 us, of 128 bytes 418 -> 330, of
+    // 256 bytes 626 -> 617, 32 query rows of them 219 -> 196.
+    const int parts = kGrid / p.kv_heads;
+    p.head_stride = parts * p.kv_heads >= 140 ? p.kv_heads : 1;
+    set_small(128);
+    e = launch_paged_few(plan->dtype, D, plan->tmK, plan->tmV, p, stream);
+  }
+  if (!few && e == cudaSuccess) {
+    // Two blocks of rows where sequences have more than one block's on average (256 rows: 218 us against 226 with one,
+    // long chunks 2290 against 2518); at D = 64 there is room for both Q blocks and deep rings anyway.
+    const bool two = D == 64 || (D == 128 && rows > (int64_t)128 * p.batch);
+    if (both) p.rows_min = kFewRows + 1;
     p.rows_max = INT32_MAX;
-    auto set_small = [&](int tk) {
-      const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
-      p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
-    };
-    // Which kernels run follows from the rows (tokens x heads of a kv head) that a sequence has on average, since its
-    // length is on the device; any lengths run on either.
-    // Up to one tile of the kernel for few rows (and the rows that a padded batch leaves free): that kernel alone.
-    // Measured, it against the other: 16 x 1 token of 16000 keys 85 against 112 us, 32 rows 219 against 249; 40 rows,
-    // its second tile reading the keys again, 393 against 259.
-    // More, in a batch of 16 or more, where there are likely to be sequences of both kinds: each on the kernel that
-    // suits its own rows (36 decoding beside 4 chunks 411 -> 403 us).  In a smaller one a launch that finds nothing
-    // costs more than that gives (4 chunks of 225 tokens 71 -> 77 us).
-    const int64_t rows = plan->n_tokens * p.group;
-    const bool can_few = p.group <= kFewRows, few = can_few && rows <= (int64_t)36 * p.batch;
-    const bool both = !few && can_few && p.batch >= 16;
-    if (few || both) {
-      if (both) p.rows_max = kFewRows;
-      p.tb = kFewRows / p.group;
-      // The heads of a token lie side by side in the cache, so they run side by side, too: CTA c takes head c % kvHeadNum.
-      // DRAM pages are then read once, and rows that end inside a line find it in L2.  Below 140 busy SMs that would
-      // cost more than it gives.  Measured with 8 kv heads, rows of 160 bytes 690 -> 427 us, of 128 bytes 418 -> 330, of
-      // 256 bytes 626 -> 617, 32 query rows of them 219 -> 196.
-      const int parts = kGrid / p.kv_heads;
-      p.head_stride = parts * p.kv_heads >= 140 ? p.kv_heads : 1;
-      set_small(128);
-      e = launch_paged_few(plan->dtype, D, plan->tmK, plan->tmV, p, stream);
-    }
-    if (!few && e == cudaSuccess) {
-      // Two blocks of rows where sequences have more than one block's on average (256 rows: 218 us against 226 with one,
-      // long chunks 2290 against 2518); at D = 64 there is room for both Q blocks and deep rings anyway.
-      const bool two = D == 64 || (D == 128 && rows > (int64_t)128 * p.batch);
-      if (both) p.rows_min = kFewRows + 1;
-      p.rows_max = INT32_MAX;
-      p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
-      p.head_stride = 1;
-      set_small(D == 256 ? 64 : 128);
-      e = launch_any(plan->dtype, D, plan->tmK, plan->tmV, p, two, stream);
-    }
+    p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
+    p.head_stride = 1;
+    set_small(D == 256 ? 64 : 128);
+    e = launch_any(plan->dtype, D, plan->tmK, plan->tmV, p, two, stream);
   }
   if (e != cudaSuccess) {
     snprintf(err, errlen, "kernel launch failed: %s", cudaGetErrorString(e));

@@ -1,4 +1,6 @@
 """Edges of the paged serving operators on the GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -79,3 +81,13 @@ def test_binding_is_refused_on_a_stream_that_is_captured():
     torch.cuda.synchronize()
     assert op.device_status() == 0
     _compare(c, out, lse)
+
+
+def test_an_execution_with_no_rows_clears_an_unbound_workspace():
+    c = paged_ref.make_case([(0, 0), (0, 50)], 4, 2, 64, BF, 16, 9, 30)
+    op, out, lse = _plan(c)
+    ws = torch.full((op.workspace_size,), 0xA5, dtype=torch.uint8, device="cuda")
+    stream, code = torch.cuda.current_stream().cuda_stream, ctypes.c_int32(-1)
+    assert ala.lib().ala_paged_attention(ws.data_ptr(), op.workspace_size, op._handle, stream) == 0
+    assert ala.lib().ala_workspace_status(op._handle, ws.data_ptr(), stream, ctypes.byref(code)) == 0
+    assert code.value == 0

@@ -425,8 +425,9 @@ ALA_API int ala_paged_write(const ala_tensor* key, int64_t keyStride, const ala_
  *             bound (ala_op_bind_workspace) an execution is one to three
  *             kernel launches; unbound, a clear of 1024 bytes precedes them.
  *             Both forms may be captured into a graph (the binding itself may
- *             not).  After a wait that ran out (0x101..0x10A) the workspace
- *             has to be bound again before it is used. */
+ *             not).  After a wait that ran out (0x101..0x10A) executions into
+ *             a bound workspace write nothing until it is bound again; an
+ *             unbound one is cleared by its next execution. */
 ALA_API int ala_paged_attention_get_workspace_size(
     const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
     const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* slopes,

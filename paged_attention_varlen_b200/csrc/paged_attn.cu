@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
     fence_mbar_init();
   }
   dependency_wait();
+  const int failed = wait_failed(p);
   find_start<TK, C::THREADS>(p, &st, red);
-  __syncthreads();
-  if (st.b < 0) {  // fewer tiles than CTAs
+  if (__syncthreads_or(failed) || st.b < 0) {  // fewer tiles than CTAs
     if (threadIdx.x == 0) p.desc[blockIdx.x].n_seg = 0;
     return;
   }

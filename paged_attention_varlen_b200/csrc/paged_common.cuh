@@ -98,6 +98,14 @@ __device__ __forceinline__ float2 unpack2(uint32_t v, __nv_bfloat16*) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t v, __half*) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 
+// Whether a wait has run out in this workspace since its status was cleared: the counters of cut items may then be left
+// half way, so that later executions write nothing (until the workspace is bound again).  One thread of a CTA reads it,
+// beside the lengths, and the CTA leaves by a vote: a CTA of the same launch may be failing meanwhile, so that two reads
+// need not agree.
+__device__ __forceinline__ int wait_failed(const PagedParams& p) {
+  return threadIdx.x == 0 && *reinterpret_cast<const volatile int*>(p.status) != 0;
+}
+
 // ---------------------------------------------------------------------------------------------- the work line
 
 // One sequence as the kernel takes it: lengths outside what the tensors hold are cut to it.  Keys stay below

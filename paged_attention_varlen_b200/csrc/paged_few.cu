@@ -428,19 +428,21 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   }
   dependency_wait();
   dependency_trigger();
+  const int failed = wait_failed(p);
   tc_fence_before();
   Start st;
+  bool stop;
   if (p.small) {
     find_start_small<128>(p, st);
-    __syncthreads();
+    stop = __syncthreads_or(failed);
   } else {
     find_start<128, C::THREADS>(p, &tab.start, tab.scan);
-    __syncthreads();
+    stop = __syncthreads_or(failed);
     st = tab.start;
   }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (st.b < 0) {  // fewer tiles than CTAs
+  if (stop || st.b < 0) {  // fewer tiles than CTAs
     if (warp == kWarpMma) tmem_dealloc(tmem, C::TMEM_COLS);
     return;
   }

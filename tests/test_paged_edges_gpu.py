@@ -91,3 +91,24 @@ def test_an_execution_with_no_rows_clears_an_unbound_workspace():
     assert ala.lib().ala_paged_attention(ws.data_ptr(), op.workspace_size, op._handle, stream) == 0
     assert ala.lib().ala_workspace_status(op._handle, ws.data_ptr(), stream, ctypes.byref(code)) == 0
     assert code.value == 0
+
+
+@pytest.mark.parametrize("lens,d", [([(1, 3000), (2, 900)], 128), ([(1, 40)] * 70, 64), ([(90, 2000), (1, 50)], 64), ([(70, 400)], 256),
+                                    ([(150, 400)] + [(1, 70)] * 20, 128)])
+def test_after_a_recorded_wait_nothing_is_written_until_the_workspace_is_bound_again(lens, d):
+    # the code is put where a wait that ran out would leave it, and the counters as a cut item would
+    c = paged_ref.make_case(lens, 8, 2, d, BF, 64, 9, 35 + d)
+    op, out, lse = _plan(c)
+    op.bind()
+    header = op.workspace[:1024].view(torch.int32)
+    header[0] = 0x105
+    header[64:64 + 148] = 1
+    op()
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    assert op.device_status() == 0x105
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    _compare(c, out, lse)
+    assert (op.workspace[:1024] == 0).all()

@@ -452,7 +452,8 @@ ALA_API int ala_paged_attention(void* workspace, uint64_t workspaceSize, ala_op*
  * normWeight  NULL or [2 * headSize] fp32, device;  normEps >= 0.
  * maskType    0 or 9;  headSize a multiple of 8 up to 128; at most 64 heads
  *             per kv head.
- * Everything else as for ala_paged_attention; a row without a key gets 0. */
+ * Everything else as for ala_paged_attention; a row without a key gets 0, and
+ * so does any row of zeros where normEps is 0. */
 ALA_API int ala_paged_diff_attention_get_workspace_size(
     const ala_tensor* query, int64_t queryStride, const ala_tensor* key, const ala_tensor* value,
     const ala_tensor* blockTables, const ala_tensor* seqLen, const ala_tensor* kvSeqLen, const ala_tensor* lambda,

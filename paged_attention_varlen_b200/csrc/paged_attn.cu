@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
               }
             }
             if (!two) ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-            post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
+            post *= inv_rms(p, ss);
           }
           T* orow = static_cast<T*>(p.out) + (token * (p.heads / 2) + oh) * p.row;
 #pragma unroll 1

@@ -51,6 +51,13 @@ struct PagedParams {
   __host__ __device__ int maps() const { return dq == row ? 1 : 2; }
 };
 
+// 1 / sqrt(mean square + eps) of a row whose squares add up to ss; 0 for a row of zeros without an epsilon (a row without
+// a key is one), which then stays zeros.  A NaN row's values are NaN without it.
+__device__ __forceinline__ float inv_rms(const PagedParams& p, float ss) {
+  const float ms = ss / static_cast<float>(p.row) + p.norm_eps;
+  return ms > 0.f ? rsqrtf(ms) : 0.f;
+}
+
 // Row of an item's partials that holds (token of the tile, head of the group without its map, map).
 __device__ __forceinline__ int partial_row(const PagedParams& p, bool two, int token, int hh, int map) {
   const int maps = p.maps();
@@ -552,7 +559,7 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
     if (p.norm_weight) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      post *= rsqrtf(ss / static_cast<float>(p.row) + p.norm_eps);
+      post *= inv_rms(p, ss);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] *= post * (p.norm_weight && col + i < p.row ? __ldg(p.norm_weight + col + i) : 1.f);

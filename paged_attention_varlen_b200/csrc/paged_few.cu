@@ -362,7 +362,7 @@ __device__ __forceinline__ void few_item(const PagedParams& p, const Walker<128>
     for (int i = 0; i < RT / 2; ++i) {
       if (i0 + i < outs) {
         float post = p.out_scale;
-        if (p.norm_weight) post *= rsqrtf(total(i0 + i) / static_cast<float>(p.row) + p.norm_eps);
+        if (p.norm_weight) post *= inv_rms(p, total(i0 + i));
 #pragma unroll
         for (int mi = 0; mi < C::MT; ++mi) {
           const int col = mi * 128 + r;

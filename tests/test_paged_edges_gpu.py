@@ -112,3 +112,33 @@ def test_after_a_recorded_wait_nothing_is_written_until_the_workspace_is_bound_a
     assert op.device_status() == 0
     _compare(c, out, lse)
     assert (op.workspace[:1024] == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------- a norm without an epsilon
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("lens", [[(2, 0), (5, 3), (1, 40)], [(60, 9), (1, 0)], [(200, 150), (3, 0)]])  # few rows, one block of rows, two
+def test_rows_without_a_key_get_zero_under_a_norm_without_an_epsilon(lens, d):
+    c = paged_ref.make_case(lens, 4, 2, d, BF, 16, 9, 60 + d, maps=2, norm=True)
+    c["eps"] = 0.0
+    op, out, _ = _plan(c)
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    keyless = torch.cat([torch.arange(n) + kv - n < 0 for n, kv in lens])
+    assert keyless.any()
+    got = out.cpu().double()
+    assert (got[keyless] == 0).all()
+    ref, _, tol, _ = paged_ref.attention(c)
+    assert ((got - ref).abs() <= tol)[~keyless].all()
+
+
+def test_values_of_zero_give_zero_under_a_norm_without_an_epsilon():
+    # whole items and items that several CTAs share
+    c = paged_ref.make_case([(1, 4000), (2, 70)], 4, 2, 64, BF, 16, 9, 70, maps=2, norm=True)
+    c["eps"] = 0.0
+    c["v"].zero_()
+    op, out, _ = _plan(c)
+    op()
+    torch.cuda.synchronize()
+    assert (out == 0).all()

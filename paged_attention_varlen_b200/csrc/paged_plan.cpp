@@ -18,6 +18,7 @@ using namespace ala;
 namespace {
 
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // keys of one request and rows of a cache: positions stay in int32
+constexpr int64_t kMaxElems = (int64_t)1 << 40;  // of a dim, a row or a stride: bytes, and sums of a few, stay in int64
 
 struct Err {
   char* buf;
@@ -34,7 +35,7 @@ struct Err {
 bool header_ok(const ala_tensor* t) {
   if (t->ndim < 1 || t->ndim > 4) return false;
   for (int i = 0; i < t->ndim; ++i)
-    if (t->dims[i] < 0 || t->dims[i] >= (int64_t)1 << 40) return false;
+    if (t->dims[i] < 0 || t->dims[i] >= kMaxElems) return false;
   return true;
 }
 
@@ -46,13 +47,20 @@ int elem_bytes(int32_t dtype) {
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Elements of a row, whose dims are t's from `first` on (one, or heads and headSize); -1 for more than can be counted.
+int64_t row_elems(const ala_tensor* t, int first) {
+  if (t->ndim == first + 1) return t->dims[first];
+  const int64_t heads = t->dims[first], d = t->dims[first + 1];
+  return heads > 0 && d > (kMaxElems - 1) / heads ? -1 : heads * d;
+}
+
 // [numBlocks, blockSize, row] or [numBlocks, blockSize, heads, headSize]
 bool cache_dims(const ala_tensor* t, int64_t* blocks, int64_t* block_size, int64_t* row) {
   if (t->ndim != 3 && t->ndim != 4) return false;
   *blocks = t->dims[0];
   *block_size = t->dims[1];
-  *row = t->ndim == 3 ? t->dims[2] : t->dims[2] * t->dims[3];
-  return *block_size > 0 && *blocks < kMaxKeys && *block_size < kMaxKeys && *blocks * *block_size <= kMaxKeys;
+  *row = row_elems(t, 2);
+  return *row >= 0 && *block_size > 0 && *blocks < kMaxKeys && *block_size < kMaxKeys && *blocks * *block_size <= kMaxKeys;
 }
 
 }  // namespace
@@ -95,7 +103,7 @@ int ala::paged_plan(PagedPlan* plan, const PagedAttnArgs& a, char* errbuf, size_
   const int64_t group = heads / kv_heads;
   if (group > 128) return fail(ALA_UNSUPPORTED, "more than %d query heads per kv head", 128 / maps);
   const int64_t stride = a.query_stride ? a.query_stride : heads * d;
-  if (stride < heads * d || stride % 8 || stride >= (int64_t)1 << 40)
+  if (stride < heads * d || stride % 8 || stride >= kMaxElems)
     return fail(ALA_INVALID_PARAM, "queryStride must be 0, or a multiple of 8 that holds a token's heads (got %lld)",
                 (long long)stride);
   // attnOut [nTokens, headNum * row] or [nTokens, headNum, row]
@@ -311,11 +319,10 @@ extern "C" int ala_paged_write(const ala_tensor* key, int64_t keyStride, const a
     int64_t row = 0;
     if (!cache_dims(caches[i], blocks + i, block_size + i, &row))
       return fail(ALA_INVALID_SHAPE, "the %s cache must be [numBlocks, blockSize, ...] with at most 2^30 rows", what);
-    if ((rows[i]->ndim != 2 && rows[i]->ndim != 3) || rows[i]->dims[0] != n ||
-        (rows[i]->ndim == 2 ? rows[i]->dims[1] : rows[i]->dims[1] * rows[i]->dims[2]) != row)
+    if ((rows[i]->ndim != 2 && rows[i]->ndim != 3) || rows[i]->dims[0] != n || row_elems(rows[i], 1) != row)
       return fail(ALA_INVALID_SHAPE, "%s must be [nTokens, ...] with the cache's rows of %lld elements", what, (long long)row);
     const int64_t stride = strides[i] ? strides[i] : row;
-    if (stride < row || stride >= (int64_t)1 << 40)
+    if (stride < row || stride >= kMaxElems)
       return fail(ALA_INVALID_PARAM, "the %s stride must be 0 or at least a row (%lld elements, got %lld)", what,
                   (long long)row, (long long)stride);
     stride_bytes[i] = stride * es;

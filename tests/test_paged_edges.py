@@ -1,4 +1,6 @@
 """Calls of the paged serving operators that are refused on the host, or decided there, without a GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -57,3 +59,28 @@ def test_calls_over_host_tensors_launch_nothing(which, stream, monkeypatch):
     with pytest.raises(ValueError):
         call(stream)
     assert not launched
+
+
+# ---------------------------------------------------------------------------------------------- sizes
+
+def _described(x, *shape):
+    """x's memory under another shape."""
+    t = ala.tensor(x)
+    t.ndim = len(shape)
+    for i, n in enumerate(shape):
+        t.dims[i] = n
+    return t
+
+
+@pytest.mark.parametrize("heads,d", [(1 << 32, 1 << 32), (1 << 39, 1 << 39), (1 << 31, 1 << 33), (1 << 20, 1 << 20)])
+def test_rows_whose_elements_cannot_be_counted_are_refused(heads, d):
+    # products of two dims of up to 2^40 pass 64 bits, some of them to a row of 0 elements
+    x, L, b = torch.zeros(64), ala.lib(), ctypes.byref
+    rows, cache, slots = _described(x, 4, heads, d), _described(x, 3, 16, heads, d), ala.tensor(_i32(4))
+    assert L.ala_paged_write(b(rows), 0, None, 0, b(slots), b(cache), None, None) == 2
+    q, half, out = _aligned(4, 8, 64), _aligned(64), _aligned(4, 8, 64)
+    ws, h = ctypes.c_uint64(0), ctypes.c_void_p(0)
+    wide = _described(half, 3, 16, heads, d)
+    st = L.ala_paged_attention_get_workspace_size(b(ala.tensor(q)), 0, b(wide), b(wide), b(ala.tensor(_i32(2, 4))), b(ala.tensor(_i32(2))),
+                                                  b(ala.tensor(_i32(2))), None, 9, 8, 2, 0.1, b(ala.tensor(out)), None, b(ws), b(h))
+    assert st == 2 and not h.value

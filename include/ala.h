@@ -385,7 +385,8 @@ ALA_API int ala_paged_step(const ala_tensor* seqLen, const ala_tensor* contextLe
  *             a mixture of theirs.
  * keyCache    [numBlocks, blockSize, row] or [numBlocks, blockSize, heads,
  *             headSize], key's dtype, at most 2^30 rows; valueCache alike
- *             (NULL with value).  Neither may overlap key or value.
+ *             (NULL with value).  Neither may share memory with another
+ *             tensor of the call (refused).
  * Asynchronous on `stream`, one launch, no workspace. */
 ALA_API int ala_paged_write(const ala_tensor* key, int64_t keyStride, const ala_tensor* value, int64_t valueStride,
                             const ala_tensor* slotMapping, ala_tensor* keyCache, ala_tensor* valueCache,

@@ -1,6 +1,7 @@
 // paged_plan.cpp -- argument checks of the paged serving operators, and the C entry points of the two that
 // need no workspace (ala_paged_step, ala_paged_write).  Nothing here reads device memory, so every refusal is
 // testable on a machine without a GPU.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -44,6 +45,17 @@ bool is_vector(const ala_tensor* t, int64_t n) { return t->ndim == 1 && t->dims[
 int elem_bytes(int32_t dtype) {
   return dtype == ALA_F32 || dtype == ALA_I32 ? 4 : dtype == ALA_F16 || dtype == ALA_BF16 ? 2 : dtype == ALA_I8 ? 1 : 0;
 }
+
+// A run of memory: `rows` rows of `row` bytes, `stride` apart (what is past 2^62 bytes, which no memory holds, is left out).
+// Two of them share some where neither is empty and each starts before the other ends.
+struct Span {
+  uint64_t at, end;
+  Span(const void* p, int64_t rows, int64_t stride, int64_t row) : at(reinterpret_cast<uintptr_t>(p)), end(at) {
+    if (rows > 0 && row > 0) end += (uint64_t)std::min((__int128)(rows - 1) * stride + row, (__int128)1 << 62);
+  }
+  Span(const void* p, int64_t bytes) : Span(p, 1, 0, bytes) {}
+  bool shares(const Span& o) const { return at < end && o.at < o.end && at < o.end && o.at < end; }
+};
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -247,15 +259,12 @@ extern "C" int ala_paged_step(const ala_tensor* seqLen, const ala_tensor* contex
   // kvSeqLen may be contextLens and freeCountOut freeCount (updated in place); every other output stands alone
   const ala_tensor* outs[] = {kvSeqLen, freeCountOut, cuSeqLen, slotMapping, positions, status, blockTables, freeBlocks};
   const ala_tensor* rest[] = {seqLen, contextLens, finished, freeCount};
-  auto bytes = [](const ala_tensor* t) {
+  auto span = [](const ala_tensor* t) {
     int64_t n = 4;
     for (int i = 0; i < t->ndim; ++i) n *= t->dims[i];
-    return n;
+    return Span(t->data, n);
   };
-  auto overlap = [&](const ala_tensor* x, const ala_tensor* y) {
-    const char *p = static_cast<const char*>(x->data), *q = static_cast<const char*>(y->data);
-    return bytes(x) > 0 && bytes(y) > 0 && p < q + bytes(y) && q < p + bytes(x);
-  };
+  auto overlap = [&](const ala_tensor* x, const ala_tensor* y) { return span(x).shares(span(y)); };
   for (size_t i = 0; i < sizeof outs / sizeof *outs; ++i) {
     for (size_t j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return fail(ALA_INVALID_PARAM, "two outputs overlap");
@@ -336,6 +345,16 @@ extern "C" int ala_paged_write(const ala_tensor* key, int64_t keyStride, const a
     return fail(ALA_INVALID_SHAPE, "the key and value caches differ in blocks");
   if (n > 0 && !slotMapping->data) return fail(ALA_NULL_REQUIRED, "slotMapping has a NULL data pointer");
   if (!aligned(slotMapping->data, 4)) return fail(ALA_INVALID_PARAM, "slotMapping is not aligned to its elements");
+  const int64_t n_slots = blocks[0] * block_size[0];
+  for (int i = 0; i < 2 && rows[i]; ++i) {
+    const Span cache(caches[i]->data, n_slots, row_bytes[i], row_bytes[i]);
+    bool shared = cache.shares(Span(slotMapping->data, 4 * n));
+    for (int j = 0; j < 2 && rows[j]; ++j) {
+      shared = shared || cache.shares(Span(rows[j]->data, n, stride_bytes[j], row_bytes[j]));
+      shared = shared || (j < i && cache.shares(Span(caches[j]->data, n_slots, row_bytes[j], row_bytes[j])));
+    }
+    if (shared) return fail(ALA_INVALID_PARAM, "the %s cache overlaps another tensor", i ? "value" : "key");
+  }
   a.key = static_cast<const uint8_t*>(key->data);
   a.value = value ? static_cast<const uint8_t*>(value->data) : nullptr;
   a.key_cache = static_cast<uint8_t*>(keyCache->data);
@@ -346,7 +365,7 @@ extern "C" int ala_paged_write(const ala_tensor* key, int64_t keyStride, const a
   a.key_row = row_bytes[0];
   a.value_row = row_bytes[1];
   a.n_tokens = n;
-  a.n_slots = blocks[0] * block_size[0];
+  a.n_slots = n_slots;
   const cudaError_t e = launch_paged_write(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(ALA_CUDA_ERROR, "%s", cudaGetErrorString(e));
   set_last_error("");

@@ -84,3 +84,28 @@ def test_rows_whose_elements_cannot_be_counted_are_refused(heads, d):
     st = L.ala_paged_attention_get_workspace_size(b(ala.tensor(q)), 0, b(wide), b(wide), b(ala.tensor(_i32(2, 4))), b(ala.tensor(_i32(2))),
                                                   b(ala.tensor(_i32(2))), None, 9, 8, 2, 0.1, b(ala.tensor(out)), None, b(ws), b(h))
     assert st == 2 and not h.value
+
+
+# ---------------------------------------------------------------------------------------------- shared memory
+
+@pytest.mark.parametrize("which", ["caches", "caches overlap", "key and its cache", "value and the key's cache", "slots"])
+def test_a_write_whose_tensors_share_memory_is_refused(which):
+    cache = torch.zeros(7, 16, 8)
+    rows = torch.zeros(4, 8)
+    a = dict(key=rows, value=torch.zeros(4, 8), key_cache=cache[:3], value_cache=cache[3:6], slots=_i32(4))
+    a.update({"caches": dict(value_cache=cache[:3]), "caches overlap": dict(value_cache=cache[2:5]),
+              "key and its cache": dict(key=cache[2, 12:]), "value and the key's cache": dict(value=cache[0, :4]),
+              "slots": dict(slots=cache[1, 3, 4:].view(torch.int32))}[which])
+    ts = [ala.tensor(a[x]) for x in ("key", "value", "slots", "key_cache", "value_cache")]
+    r = [ctypes.byref(t) for t in ts]
+    assert ala.lib().ala_paged_write(r[0], 0, r[1], 0, r[2], r[3], r[4], None) == 4, ala.lib().ala_last_error().decode()
+
+
+def test_a_write_may_take_rows_that_lie_between_others():
+    # key and value slices of one fused buffer, and the other half of the caches' storage, share no element
+    fused, cache = torch.zeros(4, 32), torch.zeros(6, 16, 8)
+    ts = [ala.tensor(x) for x in (fused[:0, :8], fused[:0, :8], _i32(0), cache[:3], cache[3:])]
+    for t, at in zip(ts, (0, 32)):
+        t.data, t.dims[0] = fused.data_ptr() + at, 0
+    r = [ctypes.byref(t) for t in ts]
+    assert ala.lib().ala_paged_write(r[0], 32, r[1], 32, r[2], r[3], r[4], None) == 0

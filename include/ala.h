@@ -407,6 +407,8 @@ ALA_API int ala_paged_write(const ala_tensor* key, int64_t keyStride, const ala_
  * maskType    0, 3, 4, 5 or 9 (0: every key; the others: key j <= i +
  *             kvSeqLen_b - seqLen_b for new token i).
  * lse         NULL or [nTokens, headNum] (or [..., 1]) fp32, device.
+ * attnOut may be the memory of a dense query; otherwise attnOut and lse share
+ * none with each other or an input (refused).
  *
  * A row without a key (kvSeqLen 0, or kvSeqLen < seqLen) gets output 0 and
  * lse -inf.  Slots past kvSeqLen may hold anything, NaN included; rows within

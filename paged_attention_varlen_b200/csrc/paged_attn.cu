@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < G; ++i) {
             const int c = c0 + i0 + i;
-            v[i] = c >= lo && c < hi ? __ldg(src + (c - lo)) : make_uint4(0, 0, 0, 0);
+            v[i] = c >= lo && c < hi ? ld_query(src + (c - lo)) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int i = 0; i < G; ++i) {

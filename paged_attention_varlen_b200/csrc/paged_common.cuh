@@ -77,6 +77,16 @@ struct ElemFmt<__nv_bfloat16> {
   static constexpr uint32_t fmt = 1;
 };
 
+// 16 bytes of a query row.  attnOut may be the same memory, which the kernel writes, so this is no read-only load (__ldg);
+// not volatile either, so that it is scheduled like one (a plain load, which stays behind the barriers before it, took
+// four chunks of 40 tokens from 23.6 to 24.5 us).  Its address comes from the lengths, which keeps it behind the
+// dependency wait.
+__device__ __forceinline__ uint4 ld_query(const uint4* p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* a) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]),
                "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])

@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
         const int lo = MAPS == 2 ? (qh & 1) * (p.dq / 8) : 0;  // map 2 in the upper half
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < rows && c >= lo && c < lo + p.dq / 8)
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (token0 + row / group) * p.q_stride + (int64_t)qh * p.dq) + (c - lo));
+          v = ld_query(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (token0 + row / group) * p.q_stride + (int64_t)qh * p.dq) + (c - lo));
         st_shared_v4(smem_addr(sQ) + (c >> 3) * C::QCB + row * 128 + (((c & 7) ^ (row & 7)) << 4), v);
       }
       __syncwarp();

@@ -168,6 +168,17 @@ int ala::paged_plan(PagedPlan* plan, const PagedAttnArgs& a, char* errbuf, size_
     for (const ala_tensor* t : {a.block_tables, a.seq_len, a.kv_seq_len, a.slopes, a.lambda, a.norm_weight, a.lse})
       if (t && !aligned(t->data, 4)) return fail(ALA_INVALID_PARAM, "a tensor is not aligned to its elements");
     if (!aligned(a.out->data, 32)) return fail(ALA_INVALID_PARAM, "attnOut must be 32-byte aligned");
+    // Outputs share no memory with anything, but for attnOut over a dense query: a row of it lies where its own query
+    // rows are, which its CTA, or all that hold a part of it, has read by then.
+    const Span out(a.out->data, n_tokens * heads * d * 2), lse(a.lse ? a.lse->data : nullptr, a.lse ? n_tokens * a.heads * 4 : 0);
+    const Span query(a.query->data, n_tokens, stride * 2, heads * d * 2), cache_k(a.key->data, nb * bs, r * 2, r * 2);
+    const Span ins[] = {cache_k, Span(a.value->data, nb * bs, vr * 2, vr * 2), Span(a.block_tables->data, batch * max_blocks * 4),
+                        Span(a.seq_len->data, batch * 4), Span(a.kv_seq_len->data, batch * 4)};
+    bool shared = out.shares(lse) || lse.shares(query) || (out.shares(query) && !(a.out->data == a.query->data && (stride == heads * d || n_tokens == 1)));
+    for (const Span& x : ins) shared = shared || out.shares(x) || lse.shares(x);
+    for (const ala_tensor* t : {a.slopes, a.lambda, a.norm_weight})
+      if (t) shared = shared || out.shares(Span(t->data, t->dims[0] * 4)) || lse.shares(Span(t->data, t->dims[0] * 4));
+    if (shared) return fail(ALA_INVALID_PARAM, "attnOut or lse overlaps another tensor (only attnOut may lie on a dense query)");
   }
   auto f32 = [](const ala_tensor* t) { return t ? static_cast<const float*>(t->data) : nullptr; };
   plan->dtype = dt;

@@ -109,3 +109,47 @@ def test_a_write_may_take_rows_that_lie_between_others():
         t.data, t.dims[0] = fused.data_ptr() + at, 0
     r = [ctypes.byref(t) for t in ts]
     assert ala.lib().ala_paged_write(r[0], 32, r[1], 32, r[2], r[3], r[4], None) == 0
+
+
+def _flat(n, dtype=torch.bfloat16):
+    return _aligned(n, dtype=dtype)
+
+
+@pytest.mark.parametrize("which", ["query, shifted", "query, strided", "key", "value", "tables", "lengths", "lse", "lse on lengths", "slopes"])
+def test_attention_whose_outputs_share_memory_is_refused(which):
+    n, heads, d = 10, 8, 64
+    size, buf = n * heads * d, _flat(2 * 6 * 16 * 2 * 64 + 64)
+    q, out, kc, vc = _flat(size).view(n, heads, d), _flat(size).view(n, heads, d), _aligned(6, 16, 2, d), _aligned(6, 16, 2, d)
+    a = dict(q=q, k_cache=kc, v_cache=vc, block_tables=_i32(3, 4), seq_len=_i32(3), kv_seq_len=_i32(3), mask_type=9, heads=heads,
+             kv_heads=2, qk_scale=0.125, out=out, lse=torch.zeros(n, heads))
+    wide = _aligned(n, 2 * heads * d)
+    ints, floats = out.view(-1).view(torch.int32), out.view(-1).view(torch.float32)
+    a.update({"query, shifted": dict(q=buf[:size].view(n, heads, d), out=buf[heads * d:size + heads * d].view(n, heads, d)),
+              "query, strided": dict(q=wide[:, :heads * d].view(n, heads, d), out=wide.view(-1)[:size].view(n, heads, d)),
+              "key": dict(k_cache=buf[:6 * 16 * 2 * d].view(6, 16, 2, d), out=buf[64:64 + size].view(n, heads, d)),
+              "value": dict(v_cache=buf[:6 * 16 * 2 * d].view(6, 16, 2, d), out=buf[:size].view(n, heads, d)),
+              "tables": dict(block_tables=ints[:12].view(3, 4)), "lengths": dict(seq_len=ints[4:7]),
+              "lse": dict(lse=floats[:n * heads].view(n, heads)), "slopes": dict(mask_type=3, slopes=floats[16:16 + heads]),
+              "lse on lengths": dict(lse=(x := torch.zeros(n, heads)), kv_seq_len=x.view(-1)[:3].view(torch.int32))}[which])
+    with pytest.raises(ala.AlaError) as e:
+        ala.plan_paged_attention(**a)
+    assert e.value.status == 4, str(e.value)
+
+
+def test_differential_attention_whose_output_shares_memory_is_refused():
+    out = _aligned(10, 8, 64)
+    a = dict(q=_aligned(10, 16, 32), k_cache=_aligned(6, 16, 4, 32), v_cache=_aligned(6, 16, 2, 64), block_tables=_i32(3, 4),
+             seq_len=_i32(3), kv_seq_len=_i32(3), lam=torch.zeros(8), mask_type=9, heads=8, kv_heads=2, qk_scale=0.125, out=out)
+    shared = out.view(-1).view(torch.float32)
+    for over in (dict(lam=shared[:8]), dict(norm_weight=shared[8:72])):
+        with pytest.raises(ala.AlaError) as e:
+            ala.plan_paged_diff_attention(**{**a, **over})
+        assert e.value.status == 4, str(e.value)
+
+
+def test_attention_may_write_over_its_dense_query():
+    q, cache = _aligned(10, 8, 64), _aligned(6, 16, 2, 64)
+    assert ala.plan_paged_attention(q, cache, cache, _i32(3, 4), _i32(3), _i32(3), 9, 8, 2, 0.125, out=q)[1] is q
+    q2 = _aligned(10, 16, 32)
+    out = q2.view(10, 8, 64)
+    ala.plan_paged_diff_attention(q2, cache.view(6, 16, 4, 32), cache, _i32(3, 4), _i32(3), _i32(3), torch.zeros(8), 9, 8, 2, 0.125, out=out)

@@ -6,7 +6,7 @@ import torch
 
 import paged_attention_varlen_b200 as ala
 import paged_ref
-from test_paged_gpu import BF, _compare, _plan
+from test_paged_gpu import BF, _compare, _dev, _plan
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +142,24 @@ def test_values_of_zero_give_zero_under_a_norm_without_an_epsilon():
     op()
     torch.cuda.synchronize()
     assert (out == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------- output over the query
+
+@pytest.mark.parametrize("lens", [[(1, 40), (1, 5000), (2, 300)], [(140, 900), (3, 20)], [(200, 3000), (33, 50)]])
+@pytest.mark.parametrize("maps,d", [(1, 64), (1, 128), (1, 256), (2, 32), (2, 64), (2, 128)])
+def test_the_output_may_lie_on_a_dense_query(maps, d, lens):
+    c = paged_ref.make_case(lens, 4, 2, d, BF, 16, 9, 100 + d, maps=maps)
+    q = _dev(c["q"])
+    common = [_dev(c[x]) for x in ("k", "v", "tables", "seq", "kv")]
+    out = q.view(q.shape[0], 4, maps * d)
+    if maps == 2:
+        op, _ = ala.plan_paged_diff_attention(q, *common, _dev(c["lam"]), 9, 4, 2, c["scale"], out=out)
+    else:
+        op, _ = ala.plan_paged_attention(q, *common, 9, 4, 2, c["scale"], out=out)
+    for _ in range(3):
+        q.copy_(c["q"])
+        op()
+        torch.cuda.synchronize()
+        assert op.device_status() == 0
+        _compare(c, out, None)

@@ -385,10 +385,9 @@ def _launch(index, stream, function, args):
         _check(status)
 
 
-def _capturing(stream) -> bool:
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
+def _capturing(index, stream) -> bool:
+    """Whether ``stream``, or the current stream of device ``index``, is being captured."""
+    with torch.cuda.device(index) if stream is None else torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
 
 
@@ -404,7 +403,7 @@ class PagedOp(Op):
         self._args = (self.workspace.data_ptr(), self.workspace_size, self._handle)
 
     def __call__(self, stream: torch.cuda.Stream | None = None):
-        if not self._bound and (self._index < 0 or not _capturing(stream)):
+        if not self._bound and (self._index < 0 or not _capturing(self._index, stream)):
             self.bind(stream)
         _launch(self._index, stream, self._execute, self._args)
         return self
@@ -412,7 +411,7 @@ class PagedOp(Op):
     def bind(self, stream: torch.cuda.Stream | None = None):
         """Clear the workspace's status words and what a wait that ran out left behind, without an execution.  Waits for
         ``stream``, which has to come after every execution and may not be capturing."""
-        if self._index >= 0 and _capturing(stream):
+        if self._index >= 0 and _capturing(self._index, stream):
             raise RuntimeError("a workspace cannot be bound while its stream is being captured")
         _launch(self._index, stream, lib().ala_op_bind_workspace,
                 (self._handle, self.workspace.data_ptr(), self.workspace_size))

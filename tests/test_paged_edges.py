@@ -153,3 +153,40 @@ def test_attention_may_write_over_its_dense_query():
     q2 = _aligned(10, 16, 32)
     out = q2.view(10, 8, 64)
     ala.plan_paged_diff_attention(q2, cache.view(6, 16, 4, 32), cache, _i32(3, 4), _i32(3), _i32(3), torch.zeros(8), 9, 8, 2, 0.125, out=out)
+
+
+# ---------------------------------------------------------------------------------------------- devices
+
+def test_whether_a_stream_is_captured_is_asked_of_the_tensors_device(monkeypatch):
+    # the current stream of the tensors' device, not of the device that happens to be current
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    bound, launched = [], []
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: index)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == 1)
+    cache = _aligned(6, 16, 2, 64)
+    for index, binds in ((1, False), (0, True)):
+        op, _ = ala.plan_paged_attention(_aligned(3, 4, 64), cache, cache, _i32(3, 4), _i32(3), _i32(3), 9, 4, 2, 0.125)
+        op._index = index
+        op._execute = lambda *a: launched.append(current[0]) or 0
+        monkeypatch.setattr(op, "bind", lambda stream: bound.append(index), raising=False)
+        op()
+        assert bound == ([index] if binds else []) and launched.pop() == index
+        bound.clear()
+        current[0] = 1 - current[0]
+        op()
+        assert bound == ([index] if binds else []) and launched.pop() == index
+        bound.clear()
+        current[0] = 0

@@ -73,7 +73,6 @@ struct Cfg {
   static constexpr uint32_t S_COL(int k) { return k * TK; }
   static constexpr uint32_t O_COL(int b) { return NBUF * TK + (NB == 2 ? b * D : 0); }
   static constexpr uint32_t TMEM_COLS = 512;
-  static_assert(SMEM + 512 <= 232448, "shared memory budget (512: the static part)");
   static_assert(SCRATCH / (NB * 4 * 32 * 4) % 32 == 0, "the joins take 32 columns at a time");
   static_assert(NBUF * TK + NB * D <= TMEM_COLS, "tensor memory budget");
 };
@@ -250,6 +249,7 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   __shared__ Start st;
   __shared__ int64_t red[2 * C::THREADS / 32];
+  static_assert(C::SMEM + sizeof(st) + sizeof(red) <= 232448, "shared memory budget");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

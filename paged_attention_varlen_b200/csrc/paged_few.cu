@@ -47,7 +47,6 @@ struct Few {
   static constexpr int SMEM = 1024 + NS * KV_BYTES + Q_BYTES + 2 * P_BYTES + N_BARS * 8 + 16;
   static constexpr uint32_t O_COL = 64, TMEM_COLS = 256;  // S^T [0, 32) and [32, 64), O^T from 64, 64 columns a tile
   static_assert(D != 64 || Q_BYTES + 2 * P_BYTES >= KV_BYTES, "behind the last V tile");
-  static_assert(SMEM + 1400 <= 232448, "shared memory budget (1400: the static part)");
 };
 
 // What the threads share about an item's rows, and the scratch of their reductions.
@@ -401,6 +400,7 @@ __global__ void __launch_bounds__(Few<T, D>::THREADS, 1)
   uint64_t* fin = o_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   __shared__ RowTables tab;
+  static_assert(C::SMEM + sizeof(RowTables) <= 232448, "shared memory budget");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

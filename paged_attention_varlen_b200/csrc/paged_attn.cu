@@ -669,9 +669,9 @@ __global__ void __launch_bounds__(Cfg<T, D, NQ>::THREADS, 1)
           meet();
           if (blk == 0 && warp_rows) {
             if (x0 == 0) {
-              const float m1 = sM[r], l1 = sM[128 + r], top = fmaxf(rs.m, m1), base = top == -INFINITY ? 0.f : top;
-              f0 = fast_exp2(rs.m - base);
-              f1 = fast_exp2(m1 - base);
+              const float m1 = sM[r], l1 = sM[128 + r], top = fmaxf(rs.m, m1);
+              f0 = fast_exp2(rs.m - top);
+              f1 = fast_exp2(m1 - top);
               rs.l = rs.l * f0 + l1 * f1;
               rs.m = top;
             }
@@ -972,10 +972,6 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
   p.box_rows = box;
   p.rows_min = 0;
   p.rows_max = INT32_MAX;
-  auto set_small = [&](int tk) {
-    const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / tk + 1) * p.kv_heads;
-    p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
-  };
   // Which kernels run follows from the rows (tokens x heads of a kv head) that a sequence has on average, since its
   // length is on the device; any lengths run on either.
   // Up to one tile of the kernel for few rows (and the rows that a padded batch leaves free): that kernel alone.
@@ -996,7 +992,8 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     // 256 bytes 626 -> 617, 32 query rows of them 219 -> 196.
     const int parts = kGrid / p.kv_heads;
     p.head_stride = parts * p.kv_heads >= 140 ? p.kv_heads : 1;
-    set_small(128);
+    const int64_t most = (p.n_tokens / p.tb + (int64_t)p.batch) * ((int64_t)p.max_blocks * p.block_size / 128 + 1) * p.kv_heads;
+    p.small = p.batch <= 64 && most < 1 << 24 && p.n_tokens < 1 << 24;
     e = launch_paged_few(plan->dtype, D, plan->tmK, plan->tmV, p, stream);
   }
   if (!few && e == cudaSuccess) {
@@ -1007,7 +1004,6 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
     p.rows_max = INT32_MAX;
     p.tb = !two ? p.tb1 : p.maps() == 2 ? 128 / (p.group / 2) : 2 * p.tb1;
     p.head_stride = 1;
-    set_small(D == 256 ? 64 : 128);
     e = launch_any(plan->dtype, D, plan->tmK, plan->tmV, p, two, stream);
   }
   if (e != cudaSuccess) {

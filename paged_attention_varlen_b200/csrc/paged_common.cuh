@@ -43,7 +43,7 @@ struct PagedParams {
   int32_t tb1, tb;                 // tokens of one block of rows (128 / group), tokens per row tile
   int32_t dq, row;                 // query head size, elements of a K / V row
   int32_t box_rows;
-  int32_t small;                   // at most 64 sequences whose lengths, whatever they are, make fewer than 2^24 tiles
+  int32_t small;                   // few rows: at most 64 sequences whose lengths, whatever they are, make fewer than 2^24 tiles
   int32_t rows_min, rows_max;      // sequences with rows (per kv head) outside this range are another launch's
   int32_t head_stride;             // 1: the line holds all kv heads; kv_heads: a line for each, CTA c on that of head c % kv_heads
   float scale_log2, norm_eps, out_scale;
@@ -517,18 +517,17 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
         if (s0 + u < d.n_seg && col < p.row) load_f<N>(p.part + (int64_t)prow(map, s0 + u) * D + col, v[map][u]);
   };
   fetch(0);
-  float top[MAPS], base[MAPS], sum[MAPS], acc[MAPS][N];
+  float top[MAPS], sum[MAPS], acc[MAPS][N];  // top is kNoKey at least, as every segment's maximum
 #pragma unroll
   for (int map = 0; map < MAPS; ++map) {
     top[map] = own[map].x;
     for (int s = lane + 32; s < d.n_seg; s += 32) top[map] = fmaxf(top[map], stat(map, s).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top[map] = fmaxf(top[map], __shfl_xor_sync(0xffffffffu, top[map], o));
-    base[map] = top[map] == -INFINITY ? 0.f : top[map];
-    sum[map] = own[map].y * fast_exp2(own[map].x - base[map]);
+    sum[map] = own[map].y * fast_exp2(own[map].x - top[map]);
     for (int s = lane + 32; s < d.n_seg; s += 32) {
       const float2 o = stat(map, s);
-      sum[map] = fmaf(o.y, fast_exp2(o.x - base[map]), sum[map]);
+      sum[map] = fmaf(o.y, fast_exp2(o.x - top[map]), sum[map]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum[map] += __shfl_xor_sync(0xffffffffu, sum[map], o);
@@ -541,7 +540,7 @@ __device__ __forceinline__ void combine_row(const PagedParams& p, const PagedDes
     if (s0 > 0) fetch(s0);
     if (s0 % 32 == 0) {
 #pragma unroll
-      for (int map = 0; map < MAPS; ++map) wt[map] = fast_exp2((s0 == 0 ? own[map] : stat(map, s0 + lane)).x - base[map]);
+      for (int map = 0; map < MAPS; ++map) wt[map] = fast_exp2((s0 == 0 ? own[map] : stat(map, s0 + lane)).x - top[map]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)

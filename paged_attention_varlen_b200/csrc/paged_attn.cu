@@ -97,12 +97,6 @@ struct RowState {
   float slope_log2;
 };
 
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Scores of the NC columns from key `first` of a row, in log2 units (raw where raw_max says so); returns their
 // maximum in log2 units.
 template <int NC>

@@ -5,6 +5,7 @@
 
 #include "../../include/ala.h"
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace ala {
 
@@ -35,9 +36,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Both kernels are programmatic dependent launches: their blocks are scheduled while the kernel before them on the
-// stream ends, and wait here until it has completed.
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Both kernels are programmatic dependent launches, and wait (dependency_wait) before they touch memory.
 
 // A warp moves n block numbers, eight loads in flight in each lane: a request of 12000 keys holds 750 blocks of 16.
 template <class Load, class Store>

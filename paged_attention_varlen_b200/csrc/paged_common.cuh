@@ -96,6 +96,12 @@ __device__ __forceinline__ void st_global_v4(void* p, const uint32_t* a) {
   asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]) : "memory");
 }
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16*) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -611,9 +617,7 @@ __device__ __forceinline__ bool wait_warp2(uint64_t* bar0, uint32_t parity0, int
 
 // ---------------------------------------------------------------------------------------------- launches
 
-// Every kernel here is a programmatic dependent launch: it is scheduled while the one before it on the stream ends,
-// and waits here, before it touches memory, until that has completed.
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Every kernel here is a programmatic dependent launch: it waits (dependency_wait) before it touches memory.
 // Lets the next such kernel be scheduled from now on (it waits all the same).
 __device__ __forceinline__ void dependency_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

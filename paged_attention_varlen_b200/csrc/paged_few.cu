@@ -75,12 +75,6 @@ __device__ __forceinline__ bool any_of_256(bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // N columns of 32-bit values from TMEM column `col` on (no wait)
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t col, uint32_t (&r)[N]) {

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_attention_varlen_b200 as ala
+import paged_ref
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -190,3 +191,46 @@ def test_whether_a_stream_is_captured_is_asked_of_the_tensors_device(monkeypatch
         assert bound == ([index] if binds else []) and launched.pop() == index
         bound.clear()
         current[0] = 0
+
+
+# ---------------------------------------------------------------------------------------------- the remainder of P
+
+def carried_bound(c, monkeypatch):
+    """(out, bound of out) where P is multiplied as its rounding and the rounding of what that dropped: with u the half step of
+    the type, the first is off by at most u p, and the second by u of that, so P by u^2 p; the output's rounding u |O| stays.
+    Everything else is paged_ref's bound (fp16 weights that are subnormal lose up to 2^-25 either way)."""
+    u = paged_ref.HALF[c["q"].dtype]
+    with monkeypatch.context() as m:
+        m.setattr(paged_ref, "HALF", {c["q"].dtype: u * u})
+        out, _, tol, _ = paged_ref.attention(c)
+    return out, tol + u * out.abs()
+
+
+def _rounded_p(c, carry):
+    """The output with P rounded as the kernels round it, all else in 64 bits; every sequence's keys in one page."""
+    maps, group, dtype, at = c["maps"], c["heads"] // c["kv_heads"], c["q"].dtype, 0
+    out = torch.zeros(int(c["seq"].sum()), c["heads"], c["v"].shape[-1], dtype=torch.float64)
+    for b, (n, kv) in enumerate(zip(c["seq"].tolist(), c["kv"].tolist())):
+        page = c["tables"][b, 0].long()
+        k, v = c["k"][page, :kv].double(), c["v"][page, :kv].double()
+        for h in range(c["heads"]):
+            for m in range(maps):
+                x = c["q"][at:at + n, h * maps + m].double() @ k[:, h // group * maps + m].T * c["scale"]
+                p = torch.exp(x - x.amax(1, keepdim=True))
+                hi = p.to(dtype).double()
+                used = hi + (p - hi).to(dtype).double() if carry else hi
+                w = 1.0 if m == 0 else -float(c["lam"][h])
+                out[at:at + n, h] += w * (used @ v[:, h // group]) / p.sum(1, keepdim=True)
+        at += n
+    return out.to(dtype).double()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("maps,d", [(1, 64), (2, 64), (1, 128), (2, 32)])
+def test_the_bound_of_a_carried_remainder_notices_its_loss(maps, d, dtype, monkeypatch):
+    c = paged_ref.make_case([(1, 20), (1, 33), (1, 60)], 8, 2, d, dtype, 64, 0, 5 + d, maps=maps)
+    c["scale"] /= 16  # small scores: their own errors are below those of P
+    ref, tol = carried_bound(c, monkeypatch)
+    assert ((_rounded_p(c, True) - ref).abs() <= tol).all()
+    lost = (_rounded_p(c, False) - ref).abs() > tol
+    assert lost.float().mean() > 0.005

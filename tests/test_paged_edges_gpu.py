@@ -6,7 +6,8 @@ import torch
 
 import paged_attention_varlen_b200 as ala
 import paged_ref
-from test_paged_gpu import BF, _compare, _dev, _plan
+from test_paged_edges import carried_bound
+from test_paged_gpu import BF, FP, _compare, _dev, _plan
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +164,23 @@ def test_the_output_may_lie_on_a_dense_query(maps, d, lens):
         torch.cuda.synchronize()
         assert op.device_status() == 0
         _compare(c, out, None)
+
+
+# ---------------------------------------------------------------------------------------------- the remainder of P
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lens,heads,kv_heads,d,maps,mask", [
+    ([(1, 60), (1, 33), (1, 128), (0, 0), (1, 7), (1, 300)], 8, 2, 64, 1, 9), ([(1, 60), (1, 33), (1, 130)], 16, 1, 128, 1, 0),
+    ([(2, 60), (2, 33), (1, 64)], 8, 1, 256, 1, 9), ([(1, 60), (1, 33), (1, 128)], 4, 4, 80, 1, 4),
+    ([(1, 60), (1, 33), (1, 128), (1, 7)], 4, 2, 64, 2, 9), ([(1, 60), (1, 40)], 16, 1, 32, 2, 0), ([(2, 60), (4, 40)], 4, 1, 128, 2, 9),
+    ([(60, 70), (1, 33)], 4, 2, 64, 2, 9), ([(150, 160)], 4, 2, 32, 2, 9), ([(40, 90)], 2, 1, 128, 2, 0)])
+def test_p_carries_what_its_rounding_drops(lens, heads, kv_heads, d, maps, mask, dtype, monkeypatch):
+    # up to 16 rows of one map, and every difference of two: held to carried_bound
+    c = paged_ref.make_case(lens, heads, kv_heads, d, dtype, 16, mask, 80 + d, maps=maps)
+    c["scale"] /= 16  # small scores: their own errors are below those of P
+    op, out, _ = _plan(c)
+    op()
+    torch.cuda.synchronize()
+    ref, tol = carried_bound(c, monkeypatch)
+    worst = ((out.cpu().double()[:len(ref)] - ref).abs() / tol).max().item()
+    assert worst <= 1.0, f"error {worst:.2f} times its bound"

@@ -184,3 +184,46 @@ def test_p_carries_what_its_rounding_drops(lens, heads, kv_heads, d, maps, mask,
     ref, tol = carried_bound(c, monkeypatch)
     worst = ((out.cpu().double()[:len(ref)] - ref).abs() / tol).max().item()
     assert worst <= 1.0, f"error {worst:.2f} times its bound"
+
+
+# ---------------------------------------------------------------------------------------------- lengths that are cut
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("shape,pad", [((1, 1, 2), 0), ((1, 1, 2), 90), ((70, 1, 90), 0), ((70, 1, 90), 14)])
+# few rows, scanned in registers and by the CTA; many rows, alone and with a launch for few
+def test_lengths_that_are_cut_spoil_their_own_rows_only(shape, pad, d):
+    n0, n1, n2 = shape
+    kv = (200, 90, 150)
+    idle = [(0, 5)] * pad
+    c = paged_ref.make_case([(n0, kv[0]), (n1, kv[1]), (n2, kv[2]), *idle], 8, 2, d, BF, 16, 9, 40 + d)
+    c["tables"][c["tables"] < 0] = 0  # every entry may be read
+    op, out, lse = _plan(c)
+    total, big = sum(shape), 2 ** 31 - 1
+    # (lengths as they lie in memory, as they count for packing, the sequences that are cut)
+    for seq, keys, packed, cut in [
+            ((n0, n1 + total, n2), kv, (n0, total - n0, 0), (1, 2)), ((-3, n1, n2), kv, (0, n1, n2), (0,)),
+            ((n0, n1, n2), (-5, kv[1], kv[2]), (n0, n1, n2), (0,)), ((n0, n1, n2), (kv[0], big, kv[2]), (n0, n1, n2), (1,)),
+            ((n0, n1, n2), (kv[0], -2 ** 31, kv[2]), (n0, n1, n2), (1,)), ((n0, n1, big), kv, (n0, n1, n2), (2,)),
+            ((big, big, big), kv, (total, 0, 0), (0, 1, 2))]:
+        op._keep[4].copy_(torch.tensor([*seq, *[0] * pad], dtype=torch.int32))
+        op._keep[5].copy_(torch.tensor([*keys, *[5] * pad], dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        op()
+        torch.cuda.synchronize()
+        assert op.device_status() == 0x10C
+        at, own = 0, torch.zeros(total, dtype=torch.bool)
+        for b, n in enumerate(packed):
+            own[at:at + n] = b not in cut
+            at += n
+        ref, lref, tol, ltol = paged_ref.attention({**c, "seq": torch.tensor([*packed, *[0] * pad])})
+        own = own[:ref.shape[0]]
+        assert ((out.cpu().double()[:len(own)] - ref).abs() <= tol)[own].all()
+        assert ((lse.cpu().double()[:len(own)] - lref).abs() <= ltol)[own].all()
+        assert (out[at:] == 7.0).all() and (lse[at:] == 7.0).all()
+    op._keep[4].copy_(c["seq"])
+    op._keep[5].copy_(c["kv"])
+    op()
+    torch.cuda.synchronize()
+    assert op.device_status() == 0
+    _compare(c, out, lse)

@@ -18,7 +18,9 @@ Each has a ``plan_*`` form that returns an object (an ``Op``, which owns its
 workspace, where the call needs one) that runs the call again on the current
 CUDA stream (``op()``), which is what the bench does.  A planned paged call
 reads its lengths on the device, so one plan, or one CUDA graph of several,
-serves every step of a server; calls of one ``Op`` must not overlap in time.
+serves every step of a server (the size of its query decides which kernel
+runs: a plan for single tokens beside one for chunks is faster than one for
+both); calls of one ``Op`` must not overlap in time.
 """
 from __future__ import annotations
 

@@ -34,7 +34,7 @@
 //
 // What bounds it: a block's chain of softmax (some 2900 cycles for 128 keys, of which 1024 to 2048 are ex2, the tensor
 // pipe's 512 to 1024 aside) and, with two S buffers, P V and the next Q K^T (1700).  The two blocks overlap; tensor
-// pipe and ex2 unit both run at 37 % of their cycles (2 x 2048 new tokens over 8000 keys), DRAM at 4 %.
+// pipe and ex2 unit both run at 38 % of their cycles (2 x 2048 new tokens over 8000 keys), DRAM at 4 %.
 // Measured: 3 chunks of up to 4096 over 20000 keys, 32 / 8 heads, d 128: 2.24 to 2.6 ms, 820 to 960 TFLOP/s, by the
 // clock that the power cap leaves.
 #include <algorithm>
@@ -48,7 +48,9 @@ namespace ala {
 
 namespace {
 
-constexpr int kCombineY = 4;               // blocks per segment list in the combine grid
+// Blocks per segment list in the combine grid.  2, 4, 8, 16 and 32 of them: 4 chunks of 115 to 150 tokens over 1100 keys
+// 61, 52, 52, 52 and 56 us, the decoding rows and chunks of D = 64 394, 392, 388, 389 and 392, long chunks alike.
+constexpr int kCombineY = 4;
 
 // The rings fill what shared memory leaves: a tile arrives a few thousand cycles after its load is issued, so
 // depth is what keeps HBM busy.
@@ -967,10 +969,13 @@ int paged_run(PagedPlan* plan, void* workspace, cudaStream_t stream, char* err, 
   p.rows_min = 0;
   p.rows_max = INT32_MAX;
   // Which kernels run follows from the rows (tokens x heads of a kv head) that a sequence has on average, since its
-  // length is on the device; any lengths run on either.
-  // Up to one tile of the kernel for few rows (and the rows that a padded batch leaves free): that kernel alone.
+  // length is on the device; any lengths run on either.  What a step needs may differ: single tokens under a plan of 4096
+  // tokens take 19, 34 and 102 us for 1, 8 and 64 requests of 1350 to 2200 keys, against 15, 23 and 88 under their own.
+  // Up to one tile of the kernel for few rows, and 4 rows for the padding of a batch: that kernel alone.
   // Measured, it against the other: 16 x 1 token of 16000 keys 85 against 112 us, 32 rows 219 against 249; 40 rows,
-  // its second tile reading the keys again, 393 against 259.
+  // its second tile reading the keys again, 393 against 259.  The 4 rows, in batches of 4, 8, 16 and 32 over 8000 keys: where
+  // they are padding 41, 66, 90 and 164 us against 54, 79, 110 and 179; where they are tokens 47, 85, 127 and 297 against
+  // 54, 81, 128 and 221.
   // More, in a batch of 16 or more, where there are likely to be sequences of both kinds: each on the kernel that
   // suits its own rows (36 decoding beside 4 chunks 411 -> 403 us).  In a smaller one a launch that finds nothing
   // costs more than that gives (4 chunks of 225 tokens 71 -> 77 us).

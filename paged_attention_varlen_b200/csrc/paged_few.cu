@@ -17,9 +17,11 @@
 // against 2700 (d = 128) that the tile takes to arrive at a CTA's share of HBM.  What is left for speed is to keep
 // loads in flight, so the rest of shared memory is one ring of K and V tiles in the order of their use (192 KB: 4.2 us
 // of HBM at a CTA's share), which also covers the change from one item to the next.  With pages of 16 rows, or row
-// tiles of 32 under ALiBi, issuing the boxes and the softmax take 1800 to 2000 cycles a tile and come to bound it.
-// Measured: 124 tokens over 9000 keys each, 32 / 8 heads, d 128: 617 us, 6.8 TB/s (a copy: 6.5 TB/s); one token over
-// 1000 keys: 9 us, the chain of its latencies.
+// tiles of 32 under ALiBi, issuing the boxes and the softmax take 1800 to 2000 cycles a tile.
+// Measured: 124 tokens over 8300 keys on average, 32 / 8 heads, d 128: 611 to 623 us, 6.8 to 6.9 TB/s (a copy: 6.5 TB/s);
+// one token over 213 keys: 9 us, the chain of its latencies.  5 tokens of 32 requests over 4700 keys, 40 / 8 heads, d 80,
+// pages of 16, ALiBi: 106 us (the bytes 59); with pages of 128 94, without ALiBi too 90; one token each 86, and 76 with
+// pages of 128 and no ALiBi.
 //
 // The line of tiles, its split over the CTAs and the partials of cut items are those of paged_attn.cu.
 //   warps 0..7  softmax (threads r and r + 128: key r of the tile, TMEM lane r, the first and the second half of

@@ -20,7 +20,8 @@ CUDA stream (``op()``), which is what the bench does.  A planned paged call
 reads its lengths on the device, so one plan, or one CUDA graph of several,
 serves every step of a server (the size of its query decides which kernel
 runs: a plan for single tokens beside one for chunks is faster than one for
-both); calls of one ``Op`` must not overlap in time.
+both); calls of one ``Op`` must not overlap in time, and a graph that holds
+one needs the ``Op``, which owns the workspace, to stay alive.
 """
 from __future__ import annotations
 

@@ -22,7 +22,7 @@ namespace {
 // between them, pushes before pops and reads of the inputs before writes of outputs that may be the same
 // memory, is a cluster barrier, so a step is one launch.
 //
-// Launch and a chain of memory latencies bound it.  Measured: 56 requests with one token each, one CTA: 6 us (2 of them
+// Launch and a chain of memory latencies bound it.  Measured: 56 requests, 48 of them with a token, one CTA: 6 us (2 of them
 // the launch).  1000 requests, 90 of them ended, 79000 tokens: 13.6 us with 16 CTAs (the largest cluster), 17 with 8,
 // 21 with one block move or token at a time.
 constexpr int kStepThreads = 1024;
